@@ -395,6 +395,103 @@ QS_API qs_status qstate_prefill_tf32_timeouts(unsigned int* count);
  * QS_ERR_INVALID_ARG before any launch. */
 QS_API qs_status qstate_prefill_tf32_wait_selfcheck(unsigned int polls, unsigned int* timed_out);
 
+/* ------------------------------------------------------------------------
+ * State cache: the tiles of one family held as a pool of SLOTS, one slot per
+ * sequence, and a batch that names the slots it works on.  A slot is `heads`
+ * consecutive tiles: tile = slot * heads + head, slots = num_tiles / heads,
+ * with the codes and scales of the layout above, so every other entry point
+ * works on the same buffers.  These calls take token-major activations in
+ * 16 or 32 bits, strided, with the q and k heads shared by consecutive
+ * groups of value heads.
+ *
+ * `slots` is a DEVICE array of int32, one per entry of the batch.  An entry
+ * whose slot is negative or not below the number of slots is skipped:
+ * nothing of it is read or written (its rows of the output keep what they
+ * held), so a captured batch of fixed size is padded with -1.  The slots of
+ * one writing call (write, step) are distinct, as its entries run at the
+ * same time: a slot named twice is left with codes of either entry, with
+ * every access in bounds.  Reading the same slot twice is fine. */
+
+/* Element types of activations and of states handed over as values. */
+typedef enum { QS_F32 = 0, QS_F16 = 1, QS_BF16 = 2 } qs_dtype;
+
+/* A token-major batch of q, k, v and o: token i's heads start stride * i
+ * elements after the pointer, heads contiguous inside a token:
+ *   q, k [tokens][qk_heads][Dk];  v, o [tokens][heads][Dv]   (dtype)
+ * Value head h uses q/k head h / (heads / qk_heads).  q, k, v and o are
+ * 16-byte aligned and so is every stride (in bytes); strides are at least
+ * one token's heads long, so q, k and v may be slices of one buffer; o
+ * overlaps none of them. */
+typedef struct {
+  int32_t tokens;   /* entries of the batch, or rows of the packed prompts */
+  int32_t heads;    /* value heads: tiles of a slot                        */
+  int32_t qk_heads; /* q and k heads; divides heads                        */
+  int32_t dtype;    /* qs_dtype of q, k, v and o                           */
+  int64_t q_stride, k_stride, v_stride, o_stride; /* elements              */
+} qs_tokens;
+
+/* Quantize the states S [n][heads][Dv][Dk] (dtype, 32-byte aligned) into the
+ * slots: the dynamic rule (scale = group max|S| / qmax, nearest rounding),
+ * bit for bit what qstate_init writes for the same values; under
+ * QS_SCALE_PERSISTENT these scales stay fixed from here on.  QS_SCALE_YOKED
+ * returns QS_ERR_UNSUPPORTED (the cache keeps no shadow). */
+QS_API qs_status qstate_cache_write(const qs_config* cfg, int heads, int n, const int32_t* slots,
+                                    const void* S, qs_dtype dtype, void* codes, float* scales,
+                                    cudaStream_t stream);
+
+/* The slots' states back as values: S_ij = c_ij * s_ig in FP32, rounded once
+ * more to nearest even for a 16-bit dtype.  S [n][heads][Dv][Dk], 32-byte
+ * aligned.  Any policy. */
+QS_API qs_status qstate_cache_read(const qs_config* cfg, int heads, int n, const int32_t* slots,
+                                   const void* codes, const float* scales, void* S, qs_dtype dtype,
+                                   cudaStream_t stream);
+
+/* One decode step of the batch's slots, one token each, as
+ * qstate_decode_step defines it on the activations' values: the same codes
+ * and scales bit for bit, o rounded to nearest even for a 16-bit dtype.
+ * alpha [tokens][heads] (scalar decay) or [tokens][heads][Dk] (diagonal) and
+ * beta [tokens][heads] are FP32 and dense.  o == NULL skips the readout (q
+ * may then be NULL).  QS_SCALE_YOKED returns QS_ERR_UNSUPPORTED. */
+QS_API qs_status qstate_cache_step(const qs_config* cfg, const qs_tokens* batch,
+                                   const int32_t* slots, void* codes, float* scales, const void* q,
+                                   const void* k, const void* v, const float* alpha,
+                                   const float* beta, void* o, cudaStream_t stream);
+
+/* Prefill of packed prompts of unequal lengths: linear attention with a
+ * decay for each head (delta = 0, scalar decay; other recurrences return
+ * QS_ERR_UNSUPPORTED and have qstate_prefill).  Prompt i is the rows
+ * starts[i] .. starts[i+1] - 1 of the batch's `tokens` rows; per head, from
+ * S = S0[i],
+ *   S_t = alpha_t S_{t-1} + beta_t v_t k_t^T,   o_t = S_t q_t,
+ * and S1[i] is the state after its last token (S0[i] for an empty prompt).
+ *   starts [sequences + 1] int32, device, non-decreasing from 0; bounds are
+ *          clamped to [0, tokens]; rows outside every prompt are not written
+ *   S0     [sequences][heads][Dv][Dk] float, or NULL for zero states; may be
+ *          the same pointer as S1
+ *   S1     the same shape, float: what qstate_cache_write quantizes
+ *   alpha, beta [tokens][heads] float, dense; alpha in [0, 1]
+ *   o      or NULL to skip the outputs (q may then be NULL)
+ * Products with 16-bit activations run on the tensor cores with FP32
+ * accumulators; the state is carried in FP32 and formed from the
+ * activations to about 2^-16 of the magnitudes summed; the operands of the
+ * outputs (the decayed scores, and the state where it is read) are rounded
+ * to dtype once.  FP32 activations run on the CUDA cores in FP32.
+ * A decay of exactly 0 forgets everything before its token; a decay below
+ * 2^-120 counts as 0.
+ *
+ * workspace: device memory of at least qstate_prefill_packed_workspace bytes
+ * (which depends on the batch's sizes alone, and grows with tokens and
+ * sequences), 256-byte aligned, contents unspecified before and after.  Calls that
+ * may overlap on the GPU, replays of captured graphs among them, need
+ * workspaces of their own. */
+QS_API qs_status qstate_prefill_packed_workspace(const qs_config* cfg, const qs_tokens* batch,
+                                                 int sequences, size_t* bytes);
+QS_API qs_status qstate_prefill_packed(const qs_config* cfg, const qs_tokens* batch, int sequences,
+                                       const int32_t* starts, const float* S0, float* S1,
+                                       const void* q, const void* k, const void* v,
+                                       const float* alpha, const float* beta, void* o,
+                                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Squared Frobenius norm of every tile of the stored state, for tracking
  * the state norm over a decode horizon (the norm inflation of per-token
  * dynamic scaling: "When Dynamic Scaling Fails", abstract and project page,

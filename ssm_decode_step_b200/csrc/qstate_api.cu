@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "../../include/qstate.h"
+#include "qstate_check.h"
 #include "qstate_fp32.cuh"
 #include "qstate_launch.h"
 #include "qstate_launch_prefill.h"
@@ -53,68 +54,7 @@ __global__ void selfcheck_kernel(unsigned long long* bad, uint32_t lo, uint32_t 
 
 namespace {
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void* p, size_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, lo + bytes};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
-
-// Field ranges of the configuration; 0 = fine, else the status to return.
-qs_status check_config(const qs_config* c) {
-  if (c == nullptr) return QS_ERR_INVALID_ARG;
-  if (c->num_tiles < 0) return QS_ERR_INVALID_ARG;
-  if (c->dk < 1 || c->dv < 1) return QS_ERR_INVALID_ARG;
-  if (c->bits != 4 && c->bits != 8) return QS_ERR_INVALID_ARG;
-  if (c->group < 1 || c->dk % c->group != 0) return QS_ERR_INVALID_ARG;
-  if (c->delta != 0 && c->delta != 1) return QS_ERR_INVALID_ARG;
-  if (c->decay != QS_DECAY_SCALAR && c->decay != QS_DECAY_DIAGONAL) return QS_ERR_INVALID_ARG;
-  if (c->policy != QS_SCALE_DYNAMIC && c->policy != QS_SCALE_PERSISTENT && c->policy != QS_SCALE_YOKED)
-    return QS_ERR_INVALID_ARG;
-  if (c->rounding != QS_ROUND_NEAREST && c->rounding != QS_ROUND_BDR) return QS_ERR_INVALID_ARG;
-  // what this build has kernels for
-  if (c->dk != 64 && c->dk != 128) return QS_ERR_UNSUPPORTED;
-  if (c->dv % 16 != 0 || c->dv > 4096) return QS_ERR_UNSUPPORTED;
-  if (static_cast<long long>(c->num_tiles) * (c->dv / 8) > 0x7fffffffLL) return QS_ERR_UNSUPPORTED;
-  if (c->group != 32 && c->group != 64 && c->group != 128) return QS_ERR_UNSUPPORTED;
-  return QS_OK;
-}
-
-struct Sizes {
-  size_t codes, scales, shadow, vec_k, vec_v, alpha, tile_scalars;
-};
-
-Sizes sizes_of(const qs_config* c) {
-  const size_t T = static_cast<size_t>(c->num_tiles);
-  Sizes s;
-  s.codes = T * c->dv * c->dk * c->bits / 8;
-  s.scales = T * c->dv * (c->dk / c->group) * sizeof(float);
-  s.shadow = c->policy == QS_SCALE_YOKED ? T * c->dv * c->dk * sizeof(float) : 0;
-  s.vec_k = T * c->dk * sizeof(float);
-  s.vec_v = T * c->dv * sizeof(float);
-  s.alpha = c->decay == QS_DECAY_DIAGONAL ? s.vec_k : T * sizeof(float);
-  s.tile_scalars = T * sizeof(float);
-  return s;
-}
-
-qs_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QS_OK : QS_ERR_CUDA; }
-
-// Written buffers must not overlap each other or any input.
-bool any_overlap(const Range* written, int nw, const Range* read, int nr) {
-  for (int i = 0; i < nw; ++i) {
-    for (int j = i + 1; j < nw; ++j)
-      if (overlap(written[i], written[j])) return true;
-    for (int j = 0; j < nr; ++j)
-      if (overlap(written[i], read[j])) return true;
-  }
-  return false;
-}
+using namespace qs;
 
 template <int BITS, int DK>
 cudaError_t dispatch_step(const qs_config* c, const qs::StepParams& p, cudaStream_t s) {

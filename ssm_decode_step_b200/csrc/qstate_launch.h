@@ -17,6 +17,10 @@ namespace qs {
 template <int BITS, int DK, int POLICY, bool BDR, bool DELTA, bool DIAG>
 cudaError_t launch_step(const StepParams& p, cudaStream_t stream);
 
+// The step on a batch of slots (qstate_cache_step).
+template <int BITS, int DK, int POLICY, bool BDR, bool DELTA, bool DIAG>
+cudaError_t launch_cache_step(StreamParams p, int tiles, int dv, cudaStream_t stream);
+
 template <int BITS, int DK>
 cudaError_t launch_readout(const StepParams& p, cudaStream_t stream);
 

@@ -132,7 +132,7 @@ cudaError_t launch_step(const StepParams& p0, cudaStream_t stream) {
     static std::once_flag flag;
     cudaError_t err = allow_smem(kernel, flag);
     if (err != cudaSuccess) return err;
-    StreamParams p;
+    StreamParams p{};
     p.codes = p0.codes;
     p.scales = p0.scales;
     p.q = p0.q;
@@ -179,6 +179,28 @@ cudaError_t launch_step(const StepParams& p0, cudaStream_t stream) {
     p.warp_bytes = L.bytes(D, p.ntv);
     return launch_warps(kernel, p, static_cast<size_t>(p.warp_bytes) * WARPS, stream);
   }
+}
+
+// The step on a batch of slots: the streamed kernel's SLOTS instances.  p
+// carries everything but the row block counts.
+template <int BITS, int DK, int POLICY, bool BDR, bool DELTA, bool DIAG>
+cudaError_t launch_cache_step(StreamParams p, int tiles, int dv, cudaStream_t stream) {
+  constexpr int RW = 32 / (DK / 32);
+  auto kernel = stream_step_kernel<BITS, DK, POLICY, BDR, DELTA, DIAG, true>;
+  static std::once_flag flag;
+  cudaError_t err = allow_smem(kernel, flag);
+  if (err != cudaSuccess) return err;
+  p.bpt = dv / RW;
+  p.nblocks = tiles * p.bpt;  // < 2^31 (checked by the caller)
+  p.two23 = 0x4B000000u;
+  const StreamLayout L(DK, DIAG, BDR && POLICY == 0, true);
+  int per_sm = 0;
+  err = resident_ctas(kernel, 32, static_cast<size_t>(L.bytes()), &per_sm);
+  if (err != cudaSuccess) return err;
+  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  long long grid = static_cast<long long>(per_sm) * device_sm_count();
+  if (grid > p.nblocks) grid = p.nblocks;
+  return launch_dependent(kernel, grid, 32, static_cast<size_t>(L.bytes()), stream, p);
 }
 
 // The Low-Rank Bypass step: the streamed bypass kernel for the steps that
@@ -273,6 +295,16 @@ cudaError_t launch_init(const float* S0, uint8_t* codes, float* scales, float* s
   template cudaError_t launch_readout<B, D>(const StepParams&, cudaStream_t);        \
   template cudaError_t launch_init<B, D>(const float*, uint8_t*, float*, float*, long long, int, \
                                          cudaStream_t);
+
+#define QS_INSTANTIATE_CACHE_STEP(B, D, P, R) \
+  template cudaError_t launch_cache_step<B, D, P, R, false, false>(StreamParams, int, int, cudaStream_t); \
+  template cudaError_t launch_cache_step<B, D, P, R, false, true>(StreamParams, int, int, cudaStream_t);  \
+  template cudaError_t launch_cache_step<B, D, P, R, true, false>(StreamParams, int, int, cudaStream_t);  \
+  template cudaError_t launch_cache_step<B, D, P, R, true, true>(StreamParams, int, int, cudaStream_t);
+
+#define QS_INSTANTIATE_CACHE(B, D)                                                         \
+  QS_INSTANTIATE_CACHE_STEP(B, D, 0, false) QS_INSTANTIATE_CACHE_STEP(B, D, 0, true)       \
+  QS_INSTANTIATE_CACHE_STEP(B, D, 1, false) QS_INSTANTIATE_CACHE_STEP(B, D, 1, true)
 
 #define QS_INSTANTIATE_LRB1(B, D, P, R, DE, DI, M) \
   template cudaError_t launch_lrb<B, D, P, R, DE, DI, M>(const LrbParams&, int, int, cudaStream_t);

@@ -40,9 +40,17 @@
 //              dequantized comparison of qstate_kernels.cuh
 //   pack       dynamic: offset-binary fields to two's complement words;
 //              persistent: saturating integer packs
+//
+// The SLOTS instances (qstate_cache_step) run the same step on a batch of
+// slots of a pool: the batch's tiles form the sequence, a tile's row blocks
+// are read and written where its slot lies (looked up one tile ahead, so
+// that the two-blocks-ahead loads know their place), and q, k, v and o are
+// token-major, in 16 or 32 bits: 16-bit k and q land raw in shared memory
+// and are widened when their tile begins, v and o are converted at use.
 #pragma once
 
 #include "qstate_kernels.cuh"
+#include "qstate_types.cuh"
 
 namespace qs {
 
@@ -58,6 +66,14 @@ namespace qs {
 #endif
 #ifndef QS_STREAM_REGS_BDR8
 #define QS_STREAM_REGS_BDR8 200
+#endif
+// The SLOTS instances keep two tiles' places as well, and spill 4 to 26 bytes
+// at 128; INT4 fits 136 (15 warps per SM), INT8 144 (14 warps).
+#ifndef QS_STREAM_REGS_SLOTS
+#define QS_STREAM_REGS_SLOTS 136
+#endif
+#ifndef QS_STREAM_REGS_SLOTS8
+#define QS_STREAM_REGS_SLOTS8 144
 #endif
 // Where the tile's key vector lives: 1 reads it from its shared-memory slot
 // at each use, 0 holds it in registers for the tile, -1 (default) does the
@@ -83,21 +99,30 @@ struct StreamParams {
   // INT4 unpack keeps it in one register and merges each field into it with
   // a single logic operation
   uint32_t two23;
+  // SLOTS only: the batch's view of the pool
+  const int32_t* slots;
+  int num_slots;
+  unsigned heads;  // tiles of a slot
+  unsigned share;  // value heads of a q/k head
+  int dtype;       // qs_dtype of q, k, v, o
+  long long q_stride, k_stride, v_stride, o_stride;  // elements between entries
 };
 
 // One warp's shared memory: two tile-vector slots (k, q, diagonal alpha and,
 // for BDR under a changing scale, sign(k) at the padded chunk stride; then
 // alpha and beta).
 struct StreamLayout {
-  int k, q, a, sk, misc, slot;
-  __host__ __device__ StreamLayout(int dk, bool diag, bool sign_k) {
+  int k, q, a, sk, misc, raw, slot;
+  // `raw16`: room for k and q as they are in memory, in 16 bits
+  __host__ __device__ StreamLayout(int dk, bool diag, bool sign_k, bool raw16 = false) {
     const int vec = (dk / 32) * kChunkStride * 4;
     int off = 0;
     k = off;    off += vec;
     q = off;    off += vec;
     a = off;    off += diag ? vec : 0;
     sk = off;   off += sign_k ? vec : 0;
-    misc = off; off += 16;
+    misc = off; off += raw16 ? 32 : 16;  // alpha, beta; then a TileAt's v and o
+    raw = off;  off += raw16 ? 4 * dk : 0;
     slot = align_up(off, 128);
   }
   __host__ __device__ int bytes() const { return 2 * slot; }
@@ -354,9 +379,25 @@ __device__ __forceinline__ void key_sign_masks(const float2 (&kk)[16], uint32_t 
   }
 }
 
+// Where the rows of one tile of a batch of slots are: row block b of the
+// batch is block b + shift of the pool.  Row r of row block b has its v and o
+// at element v + b * RW + r and o + b * RW + r, with v and o in the tile's
+// shared-memory slot.
+struct TileAt {
+  int shift;
+  bool live;  // the slot is one of the pool's; else nothing is written
+};
+__device__ __forceinline__ long long ld_shared_s64(uint32_t a) {
+  long long x;
+  asm volatile("ld.shared.s64 %0, [%1];\n" : "=l"(x) : "r"(a));
+  return x;
+}
+
 // POLICY: 0 dynamic, 1 persistent.
-template <int BITS, int DK, int POLICY, bool BDR, bool DELTA, bool DIAG>
-__global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_REGS_BDR) : QS_STREAM_REGS)
+template <int BITS, int DK, int POLICY, bool BDR, bool DELTA, bool DIAG, bool SLOTS = false>
+__global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_REGS_BDR)
+                                : !SLOTS ? QS_STREAM_REGS
+                                : BITS == 8 ? QS_STREAM_REGS_SLOTS8 : QS_STREAM_REGS_SLOTS)
     stream_step_kernel(StreamParams p) {
   static_assert(POLICY == 0 || POLICY == 1, "the yoked policy has its own kernel");
   constexpr int LPR = DK / 32;
@@ -378,7 +419,7 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
   extern __shared__ __align__(128) unsigned char smem[];
   const int lane = threadIdx.x & 31;
   const int c = lane % LPR, rr = lane / LPR;
-  const StreamLayout L(DK, DIAG, BDR_FLOAT);
+  const StreamLayout L(DK, DIAG, BDR_FLOAT, SLOTS);
   const unsigned ng = DK / p.group;
   const unsigned g = (32 * c) / p.group;
   const bool readout = p.o != nullptr;
@@ -406,7 +447,7 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
   // INT4: the first two row blocks' codes and scales toward L2 while the
   // previous kernel of the stream finishes (the INT8 instances, at their
   // register cap, would spill for it)
-  if constexpr (BITS == 4) {
+  if constexpr (BITS == 4 && !SLOTS) {
     prefetch_l2(codes_at(b0));
     prefetch_l2(scale_at(b0));
     if (b0 + 1 < b1) {
@@ -417,16 +458,77 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
   grid_dep_wait();
   grid_dep_launch();
 
+  // ---- SLOTS: the place of a tile's rows.  A skipped entry reads slot 0
+  // (in bounds, its values unused) and writes nothing.
+  const bool wide = !SLOTS || p.dtype == QS_F32;
+  auto place = [&](unsigned t) -> TileAt {
+    const unsigned entry = t / p.heads, head = t - entry * p.heads;
+    const int sl = __ldg(p.slots + entry);
+    TileAt at;
+    at.live = sl >= 0 && sl < p.num_slots;
+    const long long first = static_cast<long long>(t) * bpt;  // the tile's first row block in the batch
+    at.shift = static_cast<int>(
+        (static_cast<long long>(at.live ? sl : 0) * p.heads + head) * bpt - first);
+    return at;
+  };
+  // the element that row 0 of row block 0 would have in v or o, for tile t
+  auto base_of = [&](unsigned t, long long stride) {
+    const unsigned entry = t / p.heads, head = t - entry * p.heads;
+    return entry * stride + static_cast<long long>(head) * (bpt * RW) - static_cast<long long>(t) * bpt * RW;
+  };
+  auto load_row_block = [&](BlockIn<BITS>& in, unsigned b, const TileAt& at, long long v0) {
+    if constexpr (SLOTS) {
+      const unsigned pb = b + static_cast<unsigned>(at.shift);
+      const long long vi = v0 + static_cast<long long>(b) * RW + rr;
+      if constexpr (BITS == 4) {
+        ld_cg_v4(in.w, codes_at(pb));
+      } else {
+        ld_cg_v8(in.w, codes_at(pb));
+      }
+      in.s = ld_cg_f32(scale_at(pb));
+      // 16-bit v: the raw bits, widened at use
+      in.v = wide ? ld_nc_f32(p.v + vi)
+                  : __uint_as_float(__ldg(reinterpret_cast<const unsigned short*>(p.v) + vi));
+    } else {
+      load_block<BITS>(in, codes_at(b), scale_at(b), v_at(b));
+    }
+  };
+
   // ---- per-tile vectors: cp.async into the warp's two slots
   const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
   auto stage_tile = [&](unsigned t, int slot) {
     const uint32_t base = slots + slot * L.slot;
+    size_t kat = static_cast<size_t>(t) * DK, qat = kat;  // first element of the tile's k and q
+    if constexpr (SLOTS) {
+      if (lane == 0) {
+        long long* at = reinterpret_cast<long long*>(smem + slot * L.slot + L.misc + 16);
+        at[0] = base_of(t, p.v_stride);
+        at[1] = base_of(t, p.o_stride);
+      }
+      const unsigned entry = t / p.heads, kh = (t - entry * p.heads) / p.share;
+      kat = entry * static_cast<size_t>(p.k_stride) + kh * DK;
+      qat = entry * static_cast<size_t>(p.q_stride) + kh * DK;
+      if (!wide && lane < DK / 8) {
+        const uint32_t u = base + L.raw + 16 * lane;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(u),
+                     "l"(reinterpret_cast<const uint16_t*>(p.k) + kat + 8 * lane)
+                     : "memory");
+        if (readout)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(u + 2 * DK),
+                       "l"(reinterpret_cast<const uint16_t*>(p.q) + qat + 8 * lane)
+                       : "memory");
+      }
+    }
     if (lane < DK / 4) {
       const uint32_t u = base + static_cast<uint32_t>(vec_unit_offset(lane));
       const size_t off = static_cast<size_t>(t) * DK + 4 * lane;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(u + L.k), "l"(p.k + off) : "memory");
-      if (readout)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(u + L.q), "l"(p.q + off) : "memory");
+      if (wide) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(u + L.k), "l"(p.k + kat + 4 * lane)
+                     : "memory");
+        if (readout)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(u + L.q), "l"(p.q + qat + 4 * lane)
+                       : "memory");
+      }
       if constexpr (DIAG)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(u + L.a), "l"(p.alpha + off)
                      : "memory");
@@ -447,9 +549,18 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
   if (tile_end < b1) stage_tile(tile + 1, 1);
   cp_async_commit();
 
+  TileAt cur{}, nxt{};  // SLOTS: this tile's place and the next one's
+  if constexpr (SLOTS) {
+    cur = place(tile);
+    nxt = tile_end < b1 ? place(tile + 1) : cur;
+  }
   BlockIn<BITS> A, B;
-  load_block<BITS>(A, codes_at(b0), scale_at(b0), v_at(b0));
-  if (b0 + 1 < b1) load_block<BITS>(B, codes_at(b0 + 1), scale_at(b0 + 1), v_at(b0 + 1));
+  auto v_base = [&](int sl) { return SLOTS ? ld_shared_s64(slots + sl * L.slot + L.misc + 16) : 0ll; };
+  auto o_base = [&](int sl) { return SLOTS ? ld_shared_s64(slots + sl * L.slot + L.misc + 24) : 0ll; };
+  if constexpr (SLOTS) __syncwarp();  // the bases that lane 0 wrote
+  load_row_block(A, b0, cur, v_base(0));
+  if (b0 + 1 < b1)
+    load_row_block(B, b0 + 1, b0 + 1 < tile_end ? cur : nxt, v_base(b0 + 1 < tile_end ? 0 : 1));
 
   float2 kk[16];
   float beta = 0.0f, a_scalar = 1.0f;
@@ -457,6 +568,23 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
   const unsigned char* tv = smem;
   auto enter_tile = [&]() {
     tv = smem + slot * L.slot;
+    if constexpr (SLOTS) {
+      if (!wide) {
+        // k and q to FP32 at the padded chunk stride, four elements a lane
+        if (lane < DK / 4) {
+          auto widen = [&](int from, int to) {
+            const uint2 r = *reinterpret_cast<const uint2*>(tv + L.raw + from + 8 * lane);
+            const float2 x = p.dtype == QS_F16 ? F16::widen2(r.x) : BF16::widen2(r.x);
+            const float2 y = p.dtype == QS_F16 ? F16::widen2(r.y) : BF16::widen2(r.y);
+            *reinterpret_cast<float4*>(const_cast<unsigned char*>(tv) + to + vec_unit_offset(lane)) =
+                make_float4(x.x, x.y, y.x, y.y);
+          };
+          widen(0, L.k);
+          if (readout) widen(2 * DK, L.q);
+        }
+        __syncwarp();
+      }
+    }
     if constexpr (KS) {
       if constexpr (BDR) load_pairs(tv + L.k, c, kk);   // for the sign masks only
     } else {
@@ -494,14 +622,38 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
 #pragma unroll
       for (int q = 0; q < CW; ++q) cold[q] = in.w[q] ^ TOPS;  // offset binary
     }
-    const float s_old = in.s, v_i = in.v;
+    const float s_old = in.s;
+    float v_i = in.v;
+    if constexpr (SLOTS) {
+      if (!wide) {
+        const uint32_t raw = __float_as_uint(v_i);
+        v_i = p.dtype == QS_F16 ? F16::widen(static_cast<uint16_t>(raw)) : __uint_as_float(raw << 16);
+      }
+    }
     // BDR's reference under a changing scale: d = c * s
     float2 dref[BDR_FLOAT ? 16 : 1];
     if constexpr (BDR_FLOAT) {
 #pragma unroll
       for (int m = 0; m < 16; ++m) dref[m] = __fmul2_rn(Sp[m], f2(s_old));
     }
-    if (b + 2 < b1) load_block<BITS>(in, codes_at(b + 2), scale_at(b + 2), v_at(b + 2));
+    if (b + 2 < b1) {
+      if constexpr (SLOTS) {
+        TileAt at = cur;
+        long long v0;
+        if (b + 2 < tile_end) {
+          v0 = v_base(slot);
+        } else if (b + 2 < tile_end + bpt) {
+          at = nxt;
+          v0 = v_base(slot ^ 1);
+        } else {  // tiles of one row block
+          at = place(tile + 2);
+          v0 = base_of(tile + 2, p.v_stride);
+        }
+        load_row_block(in, b + 2, at, v0);
+      } else {
+        load_row_block(in, b + 2, cur, 0);
+      }
+    }
 
     // ---- a2: dequantize with the decayed scale, S' = c * (s * a)
     if constexpr (DIAG) {
@@ -545,7 +697,18 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
         acc.add(2 * m + 1, x[2 * m + 1], make_float2(t.z, t.w));
       }
       const float o = row_tree<LPR>(acc.sum());
-      if (c == 0) o_l[static_cast<unsigned long long>(b) * RW] = o;
+      if constexpr (SLOTS) {
+        if (c == 0 && cur.live) {
+          const long long oi = o_base(slot) + static_cast<long long>(b) * RW + rr;
+          if (wide) {
+            p.o[oi] = o;
+          } else {
+            reinterpret_cast<uint16_t*>(p.o)[oi] = p.dtype == QS_F16 ? F16::narrow(o) : BF16::narrow(o);
+          }
+        }
+      } else {
+        if (c == 0) o_l[static_cast<unsigned long long>(b) * RW] = o;
+      }
     }
 
     // ---- a7: scale; a8: round (persistent scales clamp every element: huge,
@@ -650,13 +813,18 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
 #pragma unroll
       for (int q = 0; q < CW; ++q) out[q] ^= TOPS;
     }
+    unsigned to = b;
+    if constexpr (SLOTS) {
+      if (!cur.live) return;
+      to = b + static_cast<unsigned>(cur.shift);
+    }
     if constexpr (CW == 4) {
-      st_global_v4(codes_at(b), out);
+      st_global_v4(codes_at(to), out);
     } else {
-      st_global_v8(codes_at(b), out);
+      st_global_v8(codes_at(to), out);
     }
     if constexpr (POLICY == 0) {
-      if (writes_scale) *scale_at(b) = sp;
+      if (writes_scale) *scale_at(to) = sp;
     }
   };
 
@@ -666,6 +834,10 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
       ++tile;
       tile_end += bpt;
       slot ^= 1;
+      if constexpr (SLOTS) {
+        cur = nxt;
+        if (tile_end < b1) nxt = place(tile + 1);
+      }
       cp_async_wait<0>();
       // every lane's copies of this tile have landed, and every lane is done
       // with the slot that the next tile's copies overwrite
@@ -673,6 +845,7 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
       enter_tile();
       if (tile_end < b1) stage_tile(tile + 1, slot ^ 1);
       cp_async_commit();
+      if constexpr (SLOTS) __syncwarp();
     }
   };
   unsigned b = b0;

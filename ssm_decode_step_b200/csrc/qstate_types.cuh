@@ -1,0 +1,52 @@
+// Activation and state element types of the cache and packed-prefill
+// kernels: qs_dtype tags, widening loads and rounding stores.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/qstate.h"
+
+namespace qs {
+
+inline size_t dtype_bytes(int dtype) { return dtype == QS_F32 ? 4 : 2; }
+
+// The element types as tags: `bits` is what memory holds, widen/narrow are
+// exact / rounded to nearest even.
+struct F32 {
+  using T = float;
+  static constexpr int kTag = QS_F32;
+  static __device__ __forceinline__ float widen(float x) { return x; }
+  static __device__ __forceinline__ float narrow(float x) { return x; }
+};
+struct F16 {
+  using T = uint16_t;
+  static constexpr int kTag = QS_F16;
+  static __device__ __forceinline__ float widen(uint16_t x) { return __half2float(__ushort_as_half(x)); }
+  static __device__ __forceinline__ uint16_t narrow(float x) { return __half_as_ushort(__float2half_rn(x)); }
+  // two elements of a word, the lower address in the low half
+  static __device__ __forceinline__ float2 widen2(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+  static __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+struct BF16 {
+  using T = uint16_t;
+  static constexpr int kTag = QS_BF16;
+  static __device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+  static __device__ __forceinline__ uint16_t narrow(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+  static __device__ __forceinline__ float2 widen2(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+}  // namespace qs

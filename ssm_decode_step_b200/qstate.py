@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libqstate.so")
 DECAY = {"scalar": 0, "diagonal": 1}
 POLICY = {"dynamic": 0, "persistent": 1, "yoked": 2}
 ROUNDING = {"nearest": 0, "bdr": 1}
+QS_F32, QS_F16, QS_BF16 = 0, 1, 2
 
 QS_OK, QS_ERR_INVALID_ARG, QS_ERR_UNSUPPORTED, QS_ERR_CUDA = 0, 1, 2, 3
 
@@ -31,6 +32,8 @@ EXPORTS = ("qstate_query_sizes", "qstate_init", "qstate_decode_step", "qstate_re
            "qstate_pipeline_wait_stream", "qstate_pipeline_join", "qstate_pipeline_sync",
            "qstate_pipeline_destroy", "qstate_decode_step_host_static",
            "qstate_state_sq_norms", "qstate_fp32_sq_norms",
+           "qstate_cache_write", "qstate_cache_read", "qstate_cache_step",
+           "qstate_prefill_packed_workspace", "qstate_prefill_packed",
            "qstate_selfcheck", "qstate_status_string", "qstate_version")
 
 
@@ -43,6 +46,11 @@ class QStateError(RuntimeError):
 class qs_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "num_tiles", "dk", "dv", "bits", "group", "delta", "decay", "policy", "rounding")]
+
+
+class qs_tokens(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("tokens", "heads", "qk_heads", "dtype")] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "o_stride")])
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -80,6 +88,12 @@ def lib() -> ctypes.CDLL:
         L.qstate_decode_step_host_static.argtypes = [C, P, P, P, P, P, P]
         L.qstate_state_sq_norms.argtypes = [C, P, P, P, P]
         L.qstate_fp32_sq_norms.argtypes = [C, P, P, P]
+        B = ctypes.POINTER(qs_tokens)
+        L.qstate_cache_write.argtypes = [C, ctypes.c_int, ctypes.c_int, P, P, ctypes.c_int, P, P, P]
+        L.qstate_cache_read.argtypes = [C, ctypes.c_int, ctypes.c_int, P, P, P, P, ctypes.c_int, P]
+        L.qstate_cache_step.argtypes = [C, B] + [P] * 10
+        L.qstate_prefill_packed_workspace.argtypes = [C, B, ctypes.c_int, sz]
+        L.qstate_prefill_packed.argtypes = [C, B, ctypes.c_int] + [P] * 10 + [ctypes.c_size_t, P]
         for f in (L.qstate_query_sizes, L.qstate_init, L.qstate_decode_step, L.qstate_readout,
                   L.qstate_selfcheck, L.qstate_fp32_decode_step, L.qstate_state_sq_norms,
                   L.qstate_fp32_sq_norms, L.qstate_lrb_query_sizes, L.qstate_lrb_decode_step,
@@ -87,7 +101,8 @@ def lib() -> ctypes.CDLL:
                   L.qstate_prefill_tf32_wait_selfcheck, L.qstate_pipeline_query_sizes,
                   L.qstate_pipeline_create, L.qstate_pipeline_step, L.qstate_pipeline_wait_stream,
                   L.qstate_pipeline_join, L.qstate_pipeline_sync, L.qstate_pipeline_destroy,
-                  L.qstate_decode_step_host_static):
+                  L.qstate_decode_step_host_static, L.qstate_cache_write, L.qstate_cache_read,
+                  L.qstate_cache_step, L.qstate_prefill_packed_workspace, L.qstate_prefill_packed):
             f.restype = ctypes.c_int
         L.qstate_status_string.argtypes = [ctypes.c_int]
         L.qstate_status_string.restype = ctypes.c_char_p
@@ -341,6 +356,239 @@ class QState:
     def readout(self, q, o, stream=None):
         readout(self.cfg, self.codes, self.scales, q, o, stream)
         return o
+
+
+def _dtype_tag(dtype):
+    """The qs_dtype of a torch dtype."""
+    import torch
+    tag = {torch.float32: QS_F32, torch.float16: QS_F16, torch.bfloat16: QS_BF16}.get(dtype)
+    if tag is None:
+        raise ValueError(f"float32, float16 or bfloat16 values are wanted, not {dtype}")
+    return tag
+
+
+def _check_tensor(name, t, shape, dtype, device, rows=False):
+    """t has this shape, dtype and device, contiguous (`rows`: within each row of dimension 0)."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name}: {tuple(shape)} {dtype} is wanted, not {tuple(t.shape)} {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if not (t.is_contiguous() or (rows and t[:1].is_contiguous())):
+        raise ValueError(f"{name} is not contiguous" + (" within a token" if rows else ""))
+
+
+class _OnDevice:
+    """The device of an object's buffers: made current around its launches, whose stream is the
+    given one or that device's current stream."""
+
+    def __init__(self, device):
+        import torch
+        dev = torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError(f"a CUDA device is wanted, not {dev}")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+
+    def _launch(self, what, fn, args, stream):
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        if torch.cuda.current_device() == self.device.index:
+            status = fn(*args, handle)
+        else:
+            with torch.cuda.device(self.device):
+                status = fn(*args, handle)
+        if status != QS_OK:
+            raise QStateError(status, what)
+
+    def _empty(self, shape, dtype, stream):
+        """An output that this call allocates (on the current stream) and `stream` writes."""
+        import torch
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if stream is not None:
+            t.record_stream(torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream)
+        return t
+
+
+class StateCache(_OnDevice):
+    """A pool of slots, one quantized state (`heads` tiles of cfg) per sequence, and the calls of a
+    serving loop on a batch of slots: write() quantizes states into slots, read() gives them back as
+    values, step() advances them by one token (qstate_cache_write / _read / _step).
+
+    cfg.num_tiles = slots * heads.  codes uint8 [slots, heads, dv, dk*bits/8] and scales float32
+    [slots, heads, dv, dk/group] are allocated (zero: the state 0), or given and kept.  `slots`
+    arguments are int32 tensors on the cache's device; an entry outside [0, slots) is skipped.  The
+    slots of one write or step are distinct.  Calls that overlap on the GPU may not write the
+    same slots."""
+
+    def __init__(self, cfg: Config, heads: int, device=None, codes=None, scales=None):
+        import torch
+        if codes is not None and device is None:
+            device = codes.device
+        super().__init__("cuda" if device is None else device)
+        if cfg.policy == "yoked":
+            raise ValueError("a state cache keeps no shadow: the yoked policy has QState")
+        if heads < 1 or cfg.num_tiles % heads:
+            raise ValueError(f"{heads} heads do not divide {cfg.num_tiles} tiles")
+        query_sizes(cfg)  # checks the fields
+        self.cfg, self.heads, self.slots = cfg, heads, cfg.num_tiles // heads
+        shapes = ((self.slots, heads, cfg.dv, cfg.dk * cfg.bits // 8), (self.slots, heads, cfg.dv, cfg.groups))
+        if codes is None:
+            codes = torch.zeros(shapes[0], dtype=torch.uint8, device=self.device)
+        if scales is None:
+            scales = torch.zeros(shapes[1], dtype=torch.float32, device=self.device)
+        _check_tensor("codes", codes, shapes[0], torch.uint8, self.device)
+        _check_tensor("scales", scales, shapes[1], torch.float32, self.device)
+        self.codes, self.scales = codes, scales
+        self._cc = cfg.c()
+        self._ccp = ctypes.byref(self._cc)
+
+    def _slots(self, slots):
+        import torch
+        n = slots.shape[0] if slots.dim() else -1
+        _check_tensor("slots", slots, (n,), torch.int32, self.device)
+        return n
+
+    def write(self, slots, S, stream=None) -> None:
+        """Quantize S [n, heads, dv, dk] (float32, float16 or bfloat16) into the slots."""
+        n, c = self._slots(slots), self.cfg
+        tag = _dtype_tag(S.dtype)
+        _check_tensor("S", S, (n, self.heads, c.dv, c.dk), S.dtype, self.device)
+        self._launch("qstate_cache_write", lib().qstate_cache_write,
+                     (self._ccp, self.heads, n, slots.data_ptr(), S.data_ptr(), tag, self.codes.data_ptr(),
+                      self.scales.data_ptr()), stream)
+
+    def read(self, slots, out=None, dtype=None, stream=None):
+        """The slots' states as values [n, heads, dv, dk]: into `out`, or a new tensor of `dtype`
+        (float32 by default; zeros for skipped entries)."""
+        import torch
+        n, c = self._slots(slots), self.cfg
+        if out is None:
+            out = self._empty((n, self.heads, c.dv, c.dk), torch.float32 if dtype is None else dtype, None)
+            out.zero_()
+            if stream is not None:
+                s = torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream
+                s.wait_stream(torch.cuda.current_stream(self.device))
+                out.record_stream(s)
+        tag = _dtype_tag(out.dtype)
+        _check_tensor("out", out, (n, self.heads, c.dv, c.dk), out.dtype, self.device)
+        self._launch("qstate_cache_read", lib().qstate_cache_read,
+                     (self._ccp, self.heads, n, slots.data_ptr(), self.codes.data_ptr(), self.scales.data_ptr(),
+                      out.data_ptr(), tag), stream)
+        return out
+
+    def step(self, slots, q, k, v, alpha, beta, o=None, stream=None):
+        """One token for each of the slots, in place on the pool: q, k [n, qk_heads, dk] and
+        v [n, heads, dv] in one type (rows may be strided: slices of a fused projection), alpha
+        [n, heads] (or [n, heads, dk] for diagonal decay) and beta [n, heads] float32.  q = None skips
+        the readout; otherwise o [n, heads, dv] (given, or new: its rows of skipped entries are then
+        unspecified) is returned."""
+        import torch
+        n, c, H, dev = self._slots(slots), self.cfg, self.heads, self.device
+        T = v.dtype
+        tag = _dtype_tag(T)
+        if k.dim() != 3 or k.shape[1] < 1 or H % k.shape[1]:
+            raise ValueError(f"k: [n, qk_heads, dk] with qk_heads dividing {H} is wanted, not {tuple(k.shape)}")
+        qk = (n, k.shape[1], c.dk)
+        _check_tensor("k", k, qk, T, dev, rows=True)
+        _check_tensor("v", v, (n, H, c.dv), T, dev, rows=True)
+        _check_tensor("alpha", alpha, (n, H, c.dk) if c.decay == "diagonal" else (n, H), torch.float32, dev)
+        _check_tensor("beta", beta, (n, H), torch.float32, dev)
+        if q is not None:
+            _check_tensor("q", q, qk, T, dev, rows=True)
+            if o is None:
+                o = self._empty((n, H, c.dv), T, stream)
+            _check_tensor("o", o, (n, H, c.dv), T, dev, rows=True)
+        elif o is not None:
+            raise ValueError("a readout o needs q")
+        b = _tokens(n, H, qk[1], tag, q, k, v, o, c)
+        self._launch("qstate_cache_step", lib().qstate_cache_step,
+                     (self._ccp, ctypes.byref(b), slots.data_ptr(), self.codes.data_ptr(), self.scales.data_ptr(),
+                      _ptr(q), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), beta.data_ptr(), _ptr(o)), stream)
+        return o
+
+
+def _tokens(n, heads, qk_heads, tag, q, k, v, o, cfg):
+    """qs_tokens of a batch; a batch of one token has no stride of its own."""
+    wk, wv = qk_heads * cfg.dk, heads * cfg.dv
+    at = lambda t, w: w if t is None or n <= 1 else t.stride(0)
+    return qs_tokens(n, heads, qk_heads, tag, at(q, wk), at(k, wk), at(v, wv), at(o, wv))
+
+
+class PackedPrefill(_OnDevice):
+    """Prefill of packed prompts of unequal lengths, linear attention with a decay for each head
+    (qstate_prefill_packed), with the workspace that it keeps between calls.
+
+    cfg gives dk, dv, delta (0) and decay ("scalar"); qk_heads (default: heads) divides heads.  One
+    object serves calls of up to max_tokens tokens and max_sequences prompts, one at a time: calls
+    that may overlap on the GPU, replays of captured graphs among them, need objects of their own."""
+
+    def __init__(self, cfg: Config, heads: int, qk_heads: Optional[int] = None, *, max_tokens: int,
+                 max_sequences: int, device=None):
+        import torch
+        super().__init__("cuda" if device is None else device)
+        self.cfg, self.heads, self.qk_heads = cfg, heads, heads if qk_heads is None else qk_heads
+        self.max_tokens, self.max_sequences = max_tokens, max_sequences
+        self._cc = cfg.c()
+        self._ccp = ctypes.byref(self._cc)
+        need = packed_workspace(cfg, max_tokens, heads, self.qk_heads, max_sequences)
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+
+    def run(self, starts, q, k, v, alpha, beta, S0=None, S=None, o=None, stream=None):
+        """(o, S) of the prompts starts[i]..starts[i+1]-1 (int32 [sequences + 1]) of q, k
+        [tokens, qk_heads, dk] and v [tokens, heads, dv] (one type, rows may be strided), alpha and
+        beta [tokens, heads] float32.  S0 [sequences, heads, dv, dk] float32 are the states before the
+        first tokens (None: zeros); S (new, or given, S0 itself too) the states after the last.  q =
+        None skips the outputs.  Rows of a new o outside every prompt are unspecified."""
+        import torch
+        c, H, dev = self.cfg, self.heads, self.device
+        N, T = v.shape[0], v.dtype
+        tag = _dtype_tag(T)
+        n = starts.shape[0] - 1 if starts.dim() == 1 else -1
+        if n < 0:
+            raise ValueError("starts: [sequences + 1] is wanted")
+        if N > self.max_tokens or n > self.max_sequences:
+            raise ValueError(f"{N} tokens and {n} prompts: at most {self.max_tokens} and {self.max_sequences} are "
+                             "planned for")
+        _check_tensor("starts", starts, (n + 1,), torch.int32, dev)
+        qk = (N, self.qk_heads, c.dk)
+        _check_tensor("k", k, qk, T, dev, rows=True)
+        _check_tensor("v", v, (N, H, c.dv), T, dev, rows=True)
+        _check_tensor("alpha", alpha, (N, H), torch.float32, dev)
+        _check_tensor("beta", beta, (N, H), torch.float32, dev)
+        if S0 is not None:
+            _check_tensor("S0", S0, (n, H, c.dv, c.dk), torch.float32, dev)
+        if S is None:
+            S = self._empty((n, H, c.dv, c.dk), torch.float32, stream)
+        _check_tensor("S", S, (n, H, c.dv, c.dk), torch.float32, dev)
+        if q is not None:
+            _check_tensor("q", q, qk, T, dev, rows=True)
+            if o is None:
+                o = self._empty((N, H, c.dv), T, stream)
+            _check_tensor("o", o, (N, H, c.dv), T, dev, rows=True)
+        elif o is not None:
+            raise ValueError("outputs o need q")
+        b = _tokens(N, H, self.qk_heads, tag, q, k, v, o, c)
+        self._launch("qstate_prefill_packed", lib().qstate_prefill_packed,
+                     (self._ccp, ctypes.byref(b), n, starts.data_ptr(), _ptr(S0), S.data_ptr(), _ptr(q), k.data_ptr(),
+                      v.data_ptr(), alpha.data_ptr(), beta.data_ptr(), _ptr(o), self.workspace.data_ptr(),
+                      self.workspace.numel()), stream)
+        return o, S
+
+
+def packed_workspace(cfg: Config, tokens: int, heads: int, qk_heads: int, sequences: int) -> int:
+    """Workspace bytes of a packed prefill of up to `tokens` tokens and `sequences` prompts, of any type."""
+    n, cc = ctypes.c_size_t(), cfg.c()
+    most = 0
+    for tag in (QS_F32, QS_F16, QS_BF16):
+        b = qs_tokens(tokens, heads, qk_heads, tag, qk_heads * cfg.dk, qk_heads * cfg.dk, heads * cfg.dv,
+                      heads * cfg.dv)
+        _check(lib().qstate_prefill_packed_workspace(ctypes.byref(cc), ctypes.byref(b), sequences, ctypes.byref(n)),
+               "qstate_prefill_packed_workspace")
+        most = max(most, n.value)
+    return most
 
 
 def decode_step_host_static(cfg: Config, codes, scales, shadow, host_in, host_out=None,

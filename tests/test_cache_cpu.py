@@ -1,0 +1,154 @@
+"""State cache and packed prefill: every refusal of the C entry points and of
+the Python objects, before any CUDA call (no GPU needed)."""
+import ctypes
+
+import pytest
+
+from ssm_decode_step_b200 import Config, PackedPrefill, StateCache, qstate as Q
+
+A = 1 << 32  # fake device addresses, far apart
+
+
+def _cfg(**kw):
+    base = dict(num_tiles=24, dk=128, dv=64, bits=8, group=32, delta=0, decay="scalar", policy="dynamic",
+                rounding="nearest")
+    base.update(kw)
+    return Config(**base)
+
+
+def _batch(**kw):
+    base = dict(tokens=3, heads=4, qk_heads=2, dtype=Q.QS_BF16, q_stride=256, k_stride=256, v_stride=256,
+                o_stride=256)
+    base.update(kw)
+    return Q.qs_tokens(**base)
+
+
+def _move(write, cfg=None, heads=4, n=3, dtype=Q.QS_F32, **ptrs):
+    p = dict(slots=A, S=2 * A, codes=3 * A, scales=4 * A)
+    p.update(ptrs)
+    c = (cfg or _cfg()).c()
+    if write:
+        return Q.lib().qstate_cache_write(ctypes.byref(c), heads, n, p["slots"], p["S"], dtype, p["codes"],
+                                          p["scales"], None)
+    return Q.lib().qstate_cache_read(ctypes.byref(c), heads, n, p["slots"], p["codes"], p["scales"], p["S"], dtype,
+                                     None)
+
+
+@pytest.mark.parametrize("write", [True, False])
+@pytest.mark.parametrize("bad", [
+    dict(heads=0), dict(heads=5), dict(n=-1), dict(dtype=3), dict(dtype=-1), dict(slots=None), dict(S=None),
+    dict(codes=None), dict(scales=None), dict(slots=A + 2), dict(S=2 * A + 16), dict(codes=3 * A + 16),
+    dict(scales=4 * A + 8), dict(S=3 * A + 64), dict(slots=4 * A), dict(cfg=_cfg(bits=5)), dict(cfg=_cfg(num_tiles=-4)),
+])
+def test_move_refusals(write, bad):
+    if bad == dict(slots=4 * A) and not write:
+        bad = dict(slots=2 * A)  # an output over the slots
+    assert _move(write, **bad) == Q.QS_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("write", [True, False])
+def test_move_limits(write):
+    assert _move(write, n=0) == Q.QS_OK
+    assert _move(write, cfg=_cfg(num_tiles=0)) == Q.QS_OK  # no slot: every entry is skipped
+    assert _move(write, n=(1 << 31) // 32) == Q.QS_ERR_UNSUPPORTED
+    assert _move(write, cfg=_cfg(dk=96, group=32)) == Q.QS_ERR_UNSUPPORTED
+    if write:
+        assert _move(write, cfg=_cfg(policy="yoked")) == Q.QS_ERR_UNSUPPORTED
+
+
+def _step(cfg=None, batch=None, **ptrs):
+    p = dict(slots=A, codes=2 * A, scales=3 * A, q=4 * A, k=5 * A, v=6 * A, alpha=7 * A, beta=8 * A, o=9 * A)
+    p.update(ptrs)
+    c, b = (cfg or _cfg()).c(), batch or _batch()
+    return Q.lib().qstate_cache_step(ctypes.byref(c), ctypes.byref(b), p["slots"], p["codes"], p["scales"], p["q"],
+                                     p["k"], p["v"], p["alpha"], p["beta"], p["o"], None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(tokens=-1), dict(heads=0), dict(heads=5), dict(qk_heads=0), dict(qk_heads=3), dict(dtype=3),
+    dict(q_stride=255), dict(k_stride=248), dict(v_stride=250), dict(o_stride=-256), dict(k_stride=260),
+    dict(v_stride=1 << 41),
+])
+def test_step_batch_refusals(bad):
+    assert _step(batch=_batch(**bad)) == Q.QS_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", [
+    dict(slots=None), dict(codes=None), dict(scales=None), dict(q=None), dict(k=None), dict(v=None), dict(alpha=None),
+    dict(beta=None), dict(slots=A + 1), dict(codes=2 * A + 8), dict(scales=3 * A + 4), dict(q=4 * A + 8),
+    dict(k=5 * A + 2), dict(v=6 * A + 4), dict(o=9 * A + 2), dict(alpha=7 * A + 2), dict(beta=8 * A + 1),
+    dict(o=5 * A), dict(o=2 * A + 32), dict(beta=3 * A + 16), dict(codes=A),
+])
+def test_step_pointer_refusals(bad):
+    assert _step(**bad) == Q.QS_ERR_INVALID_ARG
+
+
+def test_step_limits():
+    c, b = _cfg().c(), _batch()
+    assert Q.lib().qstate_cache_step(None, ctypes.byref(b), *[A] * 9, None) == Q.QS_ERR_INVALID_ARG
+    assert Q.lib().qstate_cache_step(ctypes.byref(c), None, *[A] * 9, None) == Q.QS_ERR_INVALID_ARG
+    assert _step(batch=_batch(tokens=0)) == Q.QS_OK
+    assert _step(cfg=_cfg(policy="yoked")) == Q.QS_ERR_UNSUPPORTED
+    assert _step(cfg=_cfg(decay="diagonal"), alpha=7 * A + 4) == Q.QS_ERR_INVALID_ARG
+    assert _step(batch=_batch(tokens=1 << 28)) == Q.QS_ERR_UNSUPPORTED
+    # q, k and v as slices of one buffer, o in the gap behind them
+    wide = _batch(q_stride=1024, k_stride=1024, v_stride=1024, o_stride=1024)
+    assert _step(batch=wide, q=4 * A, k=4 * A + 512, v=4 * A + 1024, o=4 * A + 1536) == Q.QS_ERR_INVALID_ARG
+
+
+def _packed(cfg=None, batch=None, sequences=2, bytes_=1 << 40, **ptrs):
+    p = dict(starts=A, S0=2 * A, S1=3 * A, q=4 * A, k=5 * A, v=6 * A, alpha=7 * A, beta=8 * A, o=9 * A, ws=10 * A)
+    p.update(ptrs)
+    c, b = (cfg or _cfg()).c(), batch or _batch(tokens=70)
+    return Q.lib().qstate_prefill_packed(ctypes.byref(c), ctypes.byref(b), sequences, p["starts"], p["S0"], p["S1"],
+                                         p["q"], p["k"], p["v"], p["alpha"], p["beta"], p["o"], p["ws"], bytes_, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(sequences=-1), dict(starts=None), dict(S1=None), dict(q=None), dict(k=None), dict(v=None), dict(alpha=None),
+    dict(beta=None), dict(starts=A + 2), dict(S0=2 * A + 4), dict(S1=3 * A + 8), dict(q=4 * A + 8), dict(v=6 * A + 2),
+    dict(o=9 * A + 4), dict(alpha=7 * A + 1), dict(o=3 * A + 16), dict(S1=2 * A + 16), dict(o=6 * A), dict(S1=A),
+    dict(batch=_batch(qk_heads=3)), dict(batch=_batch(dtype=7)), dict(batch=_batch(v_stride=128)),
+    dict(cfg=_cfg(dv=0)),
+])
+def test_packed_refusals(bad):
+    assert _packed(**bad) == Q.QS_ERR_INVALID_ARG
+
+
+def test_packed_limits():
+    assert _packed(cfg=_cfg(delta=1)) == Q.QS_ERR_UNSUPPORTED
+    assert _packed(cfg=_cfg(decay="diagonal")) == Q.QS_ERR_UNSUPPORTED
+    assert _packed(cfg=_cfg(dv=40)) == Q.QS_ERR_UNSUPPORTED
+    assert _packed(sequences=0) == Q.QS_OK
+    assert _packed(sequences=(1 << 31) - 1) == Q.QS_ERR_UNSUPPORTED
+
+
+def test_workspace_grows_with_the_batch():
+    sizes = [Q.packed_workspace(_cfg(), t, 4, 2, n) for t, n in ((0, 0), (1, 1), (64, 1), (1000, 1), (1000, 4),
+                                                                (30000, 4), (30000, 64))]
+    assert sizes == sorted(sizes)
+    n = ctypes.c_size_t()
+    c, b = _cfg().c(), _batch(qk_heads=3)
+    assert Q.lib().qstate_prefill_packed_workspace(ctypes.byref(c), ctypes.byref(b), 1, ctypes.byref(n)) == \
+        Q.QS_ERR_INVALID_ARG
+    need = Q.packed_workspace(_cfg(), 1 << 20, 4, 2, 1)
+    if need:
+        big = _batch(tokens=1 << 20)
+        assert _packed(batch=big, sequences=1, bytes_=need - 1) == Q.QS_ERR_INVALID_ARG
+        assert _packed(batch=big, sequences=1, ws=None) == Q.QS_ERR_INVALID_ARG
+        assert _packed(batch=big, sequences=1, ws=10 * A + 128) == Q.QS_ERR_INVALID_ARG
+
+
+def test_python_objects_refuse():
+    with pytest.raises(ValueError):
+        StateCache(_cfg(), 4, device="cpu")
+    with pytest.raises(ValueError):
+        StateCache(_cfg(), 5, device="cuda:0")
+    with pytest.raises(ValueError):
+        StateCache(_cfg(policy="yoked"), 4, device="cuda:0")
+    with pytest.raises(Q.QStateError):
+        StateCache(_cfg(dk=96), 4, device="cuda:0")
+    with pytest.raises(ValueError):
+        PackedPrefill(_cfg(), 4, max_tokens=8, max_sequences=1, device="cpu")
+    with pytest.raises(Q.QStateError):
+        PackedPrefill(_cfg(), 4, 3, max_tokens=8, max_sequences=1, device="cuda:0")

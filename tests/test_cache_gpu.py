@@ -1,0 +1,323 @@
+"""The state cache on the GPU: write, read and step on a batch of slots.
+
+Codes and scales are bit-exact against the CPU oracle (the definition of
+include/qstate.h) on the values that the 16-bit inputs stand for; read values
+and readouts are held to 64-bit arithmetic.  Tolerances: a value read back in
+t is c * s rounded to FP32 and then to t, off by at most (2^-24 + eps(t) / 2)
+of itself; a readout is an FP32 sum of Dk <= 128 products in a fixed tree of
+depth 4 + 3 + 2, off by at most 9 * 2^-24 of the sum of the products'
+magnitudes (computed in 64 bits from the state the step left before it was
+quantized, itself 4 roundings deep: 13 * 2^-24 in all, doubled for second
+order), and rounded to t."""
+import numpy as np
+import pytest
+
+from oracle import oracle as O
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+HALF = {F32: 2.0 ** -24, F16: 2.0 ** -11, BF16: 2.0 ** -8}
+
+
+def _cfg(slots, heads, dk, dv, bits, group, delta=0, decay="scalar", policy="dynamic", rounding="nearest"):
+    from ssm_decode_step_b200 import Config
+    return Config(slots * heads, dk, dv, bits, group, delta, decay, policy, rounding)
+
+
+def _ocfg(cfg, tiles):
+    return O.OracleConfig(tiles, cfg.dk, cfg.dv, cfg.bits, cfg.group, cfg.delta, cfg.decay, cfg.policy, cfg.rounding)
+
+
+def _filled(cfg, heads):
+    """A cache whose buffers hold a pattern that no test writes."""
+    from ssm_decode_step_b200 import StateCache
+    c = StateCache(cfg, heads)
+    c.codes.fill_(0x5A)
+    c.scales.fill_(7.5)
+    return c
+
+
+def _t(a, dtype=F32):
+    return torch.from_numpy(np.ascontiguousarray(a)).to("cuda", dtype)
+
+
+def _n(t):
+    return t.float().cpu().numpy()
+
+
+def _slots(rng, n, pool, skip):
+    s = rng.permutation(pool)[:n].astype(np.int32)
+    if skip:
+        s[0] = -1
+        if n > 3:
+            s[n // 2], s[n - 1] = pool, 2 ** 31 - 1
+    return s
+
+
+SHAPES = [(1, 1, 64, 16, 2, False), (1, 4, 128, 64, 3, False), (5, 3, 64, 48, 9, True), (7, 2, 128, 80, 8, True),
+          (33, 16, 128, 128, 40, True), (2, 5, 64, 208, 2, False)]
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+@pytest.mark.parametrize("bits,group", [(4, 32), (4, 64), (4, 128), (8, 32), (8, 64), (8, 128)])
+@pytest.mark.parametrize("n,heads,dk,dv,pool,skip", SHAPES)
+def test_write_and_read(n, heads, dk, dv, pool, skip, bits, group, dtype):
+    if group > dk:
+        pytest.skip("group longer than a row")
+    cfg = _cfg(pool, heads, dk, dv, bits, group)
+    rng = np.random.default_rng(n * 1000 + dk + dv + bits + group)
+    S = _t(rng.standard_normal((n, heads, dv, dk)) * 0.3, dtype)
+    S[0, 0, 0] = 0.0              # a row of zeros
+    S[0, 0, 1, 1:] = 0.0          # one value in a group, zeros in the others
+    S[0, 0, 2, ::2] *= 2.0 ** -13 # (fp16: subnormals)
+    S[0, 0, 3] = 1.0
+    S[0, 0, 3, 1::2] = 0.5        # half the largest: next to a border between two codes
+    c = _filled(cfg, heads)
+    before = c.codes.clone(), c.scales.clone()
+    slots = _slots(rng, n, pool, skip)
+    c.write(_t(slots, torch.int32), S)
+    ora = O.init(_ocfg(cfg, n * heads), _n(S).reshape(n * heads, dv, dk))
+    packed = ora.packed().reshape(n, heads, dv, -1)
+    scales = ora.scales.reshape(n, heads, dv, -1)
+    want_c, want_s = before[0].cpu().numpy().copy(), before[1].cpu().numpy().copy()
+    good = [i for i in range(n) if 0 <= slots[i] < pool]
+    for i in good:
+        want_c[slots[i]], want_s[slots[i]] = packed[i], scales[i]
+    assert np.array_equal(c.codes.cpu().numpy(), want_c)
+    assert np.array_equal(c.scales.cpu().numpy(), want_s)
+    # back, in each type; skipped entries keep what the output held
+    exact = ora.codes.reshape(n, heads, dv, dk // group, group).astype(np.float64) * scales[..., None].astype(np.float64)
+    exact = exact.reshape(n, heads, dv, dk)
+    for t in (F32, F16, BF16):
+        out = torch.full((n, heads, dv, dk), -3.0, dtype=t, device="cuda")
+        got = c.read(_t(slots, torch.int32), out).double().cpu().numpy()
+        tiny = 2.0 ** -25 if t is F16 else 0.0  # half a step of fp16's subnormals
+        for i in range(n):
+            if i in good:
+                assert (np.abs(got[i] - exact[i]) <= (2.0 ** -24 + HALF[t]) * np.abs(exact[i]) + tiny).all()
+            else:
+                assert (got[i] == -3.0).all()
+
+
+def test_write_matches_init_on_odd_values():
+    """Subnormal, huge and infinite groups: the same bytes as the quantization start writes."""
+    from ssm_decode_step_b200 import QState, StateCache
+    for bits in (4, 8):
+        cfg = _cfg(2, 2, 64, 32, bits, 32)
+        g = torch.Generator(device="cuda").manual_seed(bits)
+        S = torch.randn(2, 2, 32, 64, generator=g, device="cuda")
+        scale = torch.tensor([1e-45, 1e-42, 1e-38, 1e-30, 1.0, 1e30, 1e37, 3e38], device="cuda")
+        S *= scale.repeat(4).view(32, 1)
+        S[0, 0, 31, 5] = float("inf")
+        st = QState(cfg).init(S.view(4, 32, 64))
+        c = StateCache(cfg, 2)
+        c.write(torch.tensor([0, 1], dtype=torch.int32, device="cuda"), S)
+        keep = torch.ones(4, 32, dtype=torch.bool, device="cuda")
+        keep[0, 31] = False  # codes of a group with an infinity are unspecified
+        assert torch.equal(c.codes.view(4, 32, -1)[keep], st.codes[keep])
+        assert torch.equal(c.scales.view(4, 32, -1), st.scales)
+
+
+def _inputs(rng, n, H, Hk, cfg, dtype, fused):
+    dk, dv = cfg.dk, cfg.dv
+    mk = lambda h, d: _t(rng.standard_normal((n, h, d)), dtype)
+    q, k, v = mk(Hk, dk), _t(rng.standard_normal((n, Hk, dk)) / np.sqrt(dk), dtype), mk(H, dv)
+    if fused:  # slices of one projection's output
+        buf = torch.cat([q.flatten(1), k.flatten(1), v.flatten(1), torch.zeros(n, 16, dtype=dtype, device="cuda")], 1)
+        w = Hk * dk
+        q, k, v = buf[:, :w].view(n, Hk, dk), buf[:, w:2 * w].view(n, Hk, dk), buf[:, 2 * w:2 * w + H * dv].view(n, H, dv)
+    alpha = _t(rng.uniform(0.8, 1.0, (n, H, dk) if cfg.decay == "diagonal" else (n, H)))
+    beta = _t(rng.uniform(0.0, 1.0, (n, H)))
+    return q, k, v, alpha, beta
+
+
+def _check_steps(cfg, n, H, Hk, pool, dtype, skip, fused, steps=3, readout=True):
+    rng = np.random.default_rng(n * 31 + H + cfg.dk + cfg.dv + cfg.bits)
+    c = _filled(cfg, H)
+    slots = _slots(rng, n, pool, False)
+    S0 = (rng.standard_normal((n, H, cfg.dv, cfg.dk)) * 0.3).astype(np.float32)
+    c.write(_t(slots, torch.int32), _t(S0))
+    if skip:
+        slots = slots.copy()
+        slots[::3] = [-1, pool, -2 ** 31][n % 3]
+    good = [i for i in range(n) if 0 <= slots[i] < pool]
+    frozen_c, frozen_s = c.codes.clone(), c.scales.clone()
+    ora = O.init(_ocfg(cfg, n * H), S0.reshape(n * H, cfg.dv, cfg.dk))
+    spread = np.arange(H) // (H // Hk)
+    for _ in range(steps):
+        q, k, v, alpha, beta = _inputs(rng, n, H, Hk, cfg, dtype, fused)
+        o = torch.full((n, H, cfg.dv), -9.0, dtype=dtype, device="cuda")
+        got = c.step(_t(slots, torch.int32), q if readout else None, k, v, alpha, beta, o=o if readout else None)
+        flat = lambda x: np.ascontiguousarray(x.reshape(n * H, *x.shape[2:]))
+        qn, kn, vn, an, bn = flat(_n(q)[:, spread]), flat(_n(k)[:, spread]), flat(_n(v)), flat(_n(alpha)), flat(_n(beta))
+        # the step in 64 bits on the stored state, for the readout
+        d = ora.dequantized().astype(np.float64).reshape(n * H, cfg.dv, cfg.dk)
+        a64 = an.astype(np.float64)
+        x = d * (a64[:, None, None] if a64.ndim == 1 else a64[:, None, :])
+        mag = np.abs(x)
+        w = vn.astype(np.float64) - (np.einsum("tij,tj->ti", x, kn.astype(np.float64)) if cfg.delta else 0.0)
+        w *= bn.astype(np.float64)[:, None]
+        wmag = (np.abs(vn) + (np.einsum("tij,tj->ti", mag, np.abs(kn)) if cfg.delta else 0.0)) * bn[:, None]
+        x = x + w[..., None] * kn[:, None, :]
+        mag = mag + wmag[..., None] * np.abs(kn)[:, None, :]
+        o64 = np.einsum("tij,tj->ti", x, qn.astype(np.float64)).reshape(n, H, cfg.dv)
+        omag = np.einsum("tij,tj->ti", mag, np.abs(qn)).reshape(n, H, cfg.dv)
+        O.step(ora, qn, kn, vn, an, bn)
+        if readout:
+            go = got.double().cpu().numpy()
+            for i in range(n):
+                if i in good:
+                    # delta: the dot product u goes through w as well, so its 9 roundings count once more
+                    tol = (2 * (22 if cfg.delta else 13) * 2.0 ** -24) * omag[i] + HALF[dtype] * np.abs(o64[i]) * 1.01
+                    assert (np.abs(go[i] - o64[i]) <= tol).all()
+                else:
+                    assert (go[i] == -9.0).all()
+        else:
+            assert got is None
+        packed = ora.packed().reshape(n, H, cfg.dv, -1)
+        want_c, want_s = frozen_c.cpu().numpy().copy(), frozen_s.cpu().numpy().copy()
+        for i in good:
+            want_c[slots[i]], want_s[slots[i]] = packed[i], ora.scales.reshape(n, H, cfg.dv, -1)[i]
+        assert np.array_equal(c.codes.cpu().numpy(), want_c)
+        assert np.array_equal(c.scales.cpu().numpy(), want_s)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+@pytest.mark.parametrize("policy", ["dynamic", "persistent"])
+@pytest.mark.parametrize("rounding", ["nearest", "bdr"])
+@pytest.mark.parametrize("bits,dk", [(4, 64), (4, 128), (8, 64), (8, 128)])
+def test_step_matches_oracle(bits, dk, rounding, policy, dtype):
+    for delta, decay in ((0, "scalar"), (1, "scalar"), (0, "diagonal"), (1, "diagonal")):
+        cfg = _cfg(11, 6, dk, 48, bits, 32, delta, decay, policy, rounding)
+        _check_steps(cfg, 8, 6, 3, 11, dtype, skip=True, fused=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+@pytest.mark.parametrize("n,heads,qk,dk,dv,group,pool", [
+    (1, 1, 1, 64, 16, 64, 1),        # one row block
+    (40, 7, 1, 64, 16, 32, 64),      # tiles of one row block: the look-ahead crosses two tiles
+    (3, 5, 5, 128, 16, 128, 4),
+    (300, 4, 2, 64, 32, 32, 400),    # ranges of warps that cross many tiles and entries
+    (2, 2, 1, 128, 320, 64, 3),
+    (200, 16, 4, 128, 64, 64, 200),
+])
+def test_step_shapes(n, heads, qk, dk, dv, group, pool, dtype):
+    for policy, bits in (("dynamic", 8), ("persistent", 4)):
+        cfg = _cfg(pool, heads, dk, dv, bits, group, 1, "scalar", policy, "nearest")
+        _check_steps(cfg, n, heads, qk, pool, dtype, skip=n > 2, fused=False, steps=2)
+
+
+def test_step_without_readout():
+    cfg = _cfg(9, 4, 128, 64, 8, 32, 1)
+    _check_steps(cfg, 5, 4, 2, 9, BF16, skip=True, fused=True, readout=False)
+
+
+def test_every_entry_skipped():
+    cfg = _cfg(4, 2, 64, 32, 4, 32)
+    c = _filled(cfg, 2)
+    codes, scales = c.codes.clone(), c.scales.clone()
+    slots = torch.tensor([-1, 4, -7], dtype=torch.int32, device="cuda")
+    z = torch.ones(3, 2, 64, device="cuda")
+    c.step(slots, z, z, z[..., :32].contiguous(), z[..., 0].contiguous(), z[..., 0].contiguous())
+    c.write(slots, torch.ones(3, 2, 32, 64, device="cuda"))
+    assert torch.equal(c.codes, codes) and torch.equal(c.scales, scales)
+    assert (c.read(slots, dtype=BF16) == 0).all()
+    none = slots[:0]
+    e = torch.empty
+    assert c.step(none, z[:0], z[:0], e(0, 2, 32, device="cuda"), e(0, 2, device="cuda"),
+                  e(0, 2, device="cuda")).shape == (0, 2, 32)
+    c.write(none, e(0, 2, 32, 64, device="cuda"))
+    assert c.read(none).shape == (0, 2, 32, 64)
+    torch.cuda.synchronize()
+
+
+def test_offsets_beyond_32_bits():
+    """A pool of 5 GB: slots whose codes start behind 2^32 bytes."""
+    pool, H = 20000, 16
+    cfg = _cfg(pool, H, 128, 128, 8, 32, 1)
+    from ssm_decode_step_b200 import StateCache
+    c = StateCache(cfg, H)
+    small = StateCache(_cfg(3, H, 128, 128, 8, 32, 1), H)
+    slots = torch.tensor([19999, 17000, 16500], dtype=torch.int32, device="cuda")
+    here = torch.arange(3, dtype=torch.int32, device="cuda")
+    rng = np.random.default_rng(3)
+    S = _t(rng.standard_normal((3, H, 128, 128)), BF16)
+    c.write(slots, S)
+    small.write(here, S)
+    q, k, v, alpha, beta = _inputs(rng, 3, H, 8, cfg, BF16, True)
+    o = c.step(slots, q, k, v, alpha, beta)
+    assert torch.equal(o, small.step(here, q, k, v, alpha, beta))
+    assert torch.equal(c.codes[slots.long()], small.codes) and torch.equal(c.scales[slots.long()], small.scales)
+    assert torch.equal(c.read(slots, dtype=F16), small.read(here, dtype=F16))
+    c.codes[slots.long()] = 0
+    assert not c.codes.view(-1, 1 << 20).any()
+
+
+def test_captured_step_follows_its_slots_and_streams():
+    """A captured batch padded with -1 is replayed on other slots; the same on a side stream."""
+    pool, H, n = 6, 4, 4
+    cfg = _cfg(pool, H, 64, 64, 8, 64, 1, policy="persistent")
+    from ssm_decode_step_b200 import StateCache
+    rng = np.random.default_rng(9)
+    S = _t(rng.standard_normal((pool, H, 64, 64)))
+    every = torch.arange(pool, dtype=torch.int32, device="cuda")
+    a, b = StateCache(cfg, H), StateCache(cfg, H)
+    a.write(every, S)
+    b.write(every, S)
+    q, k, v, alpha, beta = _inputs(rng, n, H, 2, cfg, BF16, True)
+    o = torch.zeros(n, H, 64, dtype=BF16, device="cuda")
+    slots = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a.step(slots, q, k, v, alpha, beta, o=o)  # nothing: every entry is skipped
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.step(slots, q, k, v, alpha, beta, o=o)
+    for batch in ([3, 0, -1, -1], [5, 1, 0, 2], [-1, -1, 4, -1]):
+        slots.copy_(torch.tensor(batch, dtype=torch.int32))
+        g.replay()
+        live = [i for i, s in enumerate(batch) if s >= 0]
+        with torch.cuda.stream(side):
+            side.wait_stream(torch.cuda.current_stream())
+            ref = b.step(slots, q, k, v, alpha, beta)
+        torch.cuda.synchronize()
+        assert torch.equal(o[live], ref[live])
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+    ref = b.step(slots, q, k, v, alpha, beta, stream=side)  # a stream given, outputs made by the call
+    torch.cuda.synchronize()
+    assert torch.equal(ref[2], a.step(slots, q, k, v, alpha, beta)[2])
+
+
+def test_refusals_of_the_python_calls():
+    cfg = _cfg(4, 2, 64, 32, 8, 32)
+    from ssm_decode_step_b200 import QStateError, StateCache
+    c = StateCache(cfg, 2)
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    S = torch.zeros(1, 2, 32, 64, device="cuda")
+    for bad in (one.long(), one.cpu(), torch.zeros((), dtype=torch.int32, device="cuda")):
+        with pytest.raises(ValueError):
+            c.write(bad, S)
+    for bad in (S[:, :1], S.double(), S.cpu(), S.transpose(2, 3), torch.zeros(2, 2, 32, 64, device="cuda")):
+        with pytest.raises(ValueError):
+            c.write(one, bad)
+        with pytest.raises(ValueError):
+            c.read(one, out=bad)
+    x = torch.zeros(1, 2, 64, device="cuda")
+    v, g = torch.zeros(1, 2, 32, device="cuda"), torch.ones(1, 2, device="cuda")
+    good = dict(q=x, k=x, v=v, alpha=g, beta=g)
+    for name, bad in (("q", x.half()), ("k", x[..., :32]), ("v", v.bfloat16()), ("alpha", g.half()), ("beta", g.t()),
+                      ("k", torch.zeros(1, 3, 64, device="cuda")), ("alpha", torch.ones(1, 2, 64, device="cuda")),
+                      ("v", v.cpu()), ("q", torch.zeros(2, 2, 64, device="cuda"))):
+        with pytest.raises(ValueError):
+            c.step(one, **{**good, name: bad})
+    with pytest.raises(ValueError):
+        c.step(one, **{**good, "q": None}, o=v)
+    buf = torch.zeros(2 * 2 * 64 + 8, device="cuda")
+    with pytest.raises(QStateError):  # an address off by 4 bytes
+        c.step(one, **{**good, "k": buf[1:129].view(1, 2, 64)})
+    with pytest.raises(QStateError):  # o over v
+        c.step(one, **good, o=v)

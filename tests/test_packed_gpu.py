@@ -1,0 +1,318 @@
+"""Packed prefill on the GPU, against the recurrence in 64 bits.
+
+Tolerances.  Let |S|, |o| be the same recurrence run on the magnitudes of its
+inputs (the sum of the magnitudes of every term).  A state term is a product
+of FP32 factors with one operand kept to 2^-16 of itself, and is decayed by a
+product of alphas formed through their logarithms: a prompt of n tokens sums
+at most n logarithms, each off by 2^-23 of itself, of terms whose decay is
+still worth keeping (|log2| <= 24 + log2 n matters to FP32), so the decay is
+off by less than 2^-23 * 40 * ln 2 < 2^-18; FP32 accumulation adds at most
+(64 + chunks) * 2^-24 <= 2^-15 for the lengths here up to 30000.  Together
+below 2^-14 of |S| (long) and 2^-15.4 (short): 2^-14 is asserted.  An output
+term is rounded once to the activations' type (half a step, eps / 2) where
+the state is read or the decayed score is formed, and the result once more.
+FP32 activations: no such rounding."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+HALF = {F32: 0.0, F16: 2.0 ** -11, BF16: 2.0 ** -8}
+STATE = 2.0 ** -14
+
+
+def _cfg(dk, dv):
+    from ssm_decode_step_b200 import Config
+    return Config(0, dk, dv, 8, 32, 0)
+
+
+def _recurrence(starts, q, k, v, alpha, beta, S0, share):
+    """o, S of each prompt, token by token in 64 bits (CPU or GPU tensors)."""
+    q, k = (x.double().repeat_interleave(share, 1) for x in (q, k))
+    v, alpha, beta = v.double(), alpha.double(), beta.double()
+    o = torch.zeros(v.shape[0], v.shape[1], v.shape[2], dtype=torch.float64, device=v.device)
+    n = len(starts) - 1
+    S = torch.zeros(n, v.shape[1], v.shape[2], q.shape[2], dtype=torch.float64, device=v.device)
+    if S0 is not None:
+        S.copy_(S0)
+    longest = max([b - a for a, b in zip(starts, starts[1:])] + [0])
+    for t in range(longest):
+        live = [i for i in range(n) if starts[i] + t < starts[i + 1]]
+        rows = torch.tensor([starts[i] + t for i in live], device=v.device)
+        at = torch.tensor(live, device=v.device)
+        s = S[at] * alpha[rows][..., None, None] + (beta[rows][..., None] * v[rows])[..., None] * k[rows][:, :, None, :]
+        S[at] = s
+        o[rows] = (s @ q[rows][..., None])[..., 0]
+    return o, S
+
+
+def _make(rng, lens, H, Hk, dk, dv, dtype, tail=5, decay=(0.8, 1.0), std=1.0):
+    N = sum(lens) + tail
+    t = lambda *s: torch.from_numpy(rng.standard_normal(s))
+    q, k, v = t(N, Hk, dk) * dk ** -0.5, t(N, Hk, dk) * dk ** -0.5, t(N, H, dv) * std
+    alpha = torch.from_numpy(rng.uniform(*decay, (N, H)))
+    beta = torch.from_numpy(rng.uniform(0.0, 1.0, (N, H)))
+    S0 = t(len(lens), H, dv, dk) * 0.5 * std
+    starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    c = lambda x, d: x.to("cuda", d)
+    return starts, c(q, dtype), c(k, dtype), c(v, dtype), c(alpha, F32), c(beta, F32), c(S0, F32)
+
+
+def _compare(got_o, got_S, starts, q, k, v, alpha, beta, S0, share, dtype, state=STATE):
+    o, S = _recurrence(list(starts), q, k, v, alpha, beta, S0, share)
+    om, Sm = _recurrence(list(starts), q.abs(), k.abs(), v.abs(), alpha, beta.abs(), None if S0 is None else S0.abs(),
+                         share)
+    if got_S is not None:
+        err = (got_S.double() - S).abs()
+        assert (err <= state * Sm + 1e-30).all(), float((err / (Sm + 1e-30)).max())
+    if got_o is not None:
+        end = int(starts[-1])
+        h = HALF[dtype]
+        tol = (h * (1 + h) + state) * om + max(h, 2.0 ** -24) * o.abs() + (2.0 ** -25 if dtype is F16 else 0.0)
+        err = (got_o.double() - o).abs()[:end]
+        assert (err <= tol[:end] + 1e-30).all(), float((err - tol[:end]).max())
+
+
+def _run(starts, q, k, v, alpha, beta, S0, dk, dv, **kw):
+    from ssm_decode_step_b200 import PackedPrefill
+    p = PackedPrefill(_cfg(dk, dv), v.shape[1], k.shape[1], max_tokens=v.shape[0], max_sequences=len(starts) - 1)
+    return p.run(torch.from_numpy(starts).cuda(), q, k, v, alpha, beta, S0=S0, **kw)
+
+
+LENGTHS = {
+    "one": [1], "two": [2], "chunk-1": [63], "chunk": [64], "chunk+1": [65], "long": [1000],
+    "ragged": [0, 1, 130, 0, 64, 17, 300, 63, 5, 0], "many": [7] * 50, "empty": [0, 0],
+}
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+@pytest.mark.parametrize("lens", LENGTHS, ids=str)
+@pytest.mark.parametrize("dk,dv,H,Hk", [(64, 64, 4, 4), (128, 128, 4, 2), (128, 64, 6, 1), (64, 128, 2, 1)])
+def test_matches_recurrence(dk, dv, H, Hk, lens, dtype):
+    lens = LENGTHS[lens]
+    rng = np.random.default_rng(sum(lens) + dk + dv)
+    starts, q, k, v, alpha, beta, S0 = _make(rng, lens, H, Hk, dk, dv, dtype)
+    for s0 in (S0, None):
+        S = torch.full_like(S0, 7.0)
+        o = torch.full_like(v, -5.0)
+        _run(starts, q, k, v, alpha, beta, s0, dk, dv, S=S, o=o)
+        _compare(o, S, starts, q, k, v, alpha, beta, s0, H // Hk, dtype)
+        assert (o[int(starts[-1]):] == -5.0).all()  # rows behind the last prompt
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+@pytest.mark.parametrize("dk,dv", [(64, 16), (128, 48), (64, 80), (128, 112), (128, 144), (64, 256), (128, 400)])
+def test_row_counts(dk, dv, dtype):
+    rng = np.random.default_rng(dv)
+    starts, q, k, v, alpha, beta, S0 = _make(rng, [70, 3, 129], 3, 1, dk, dv, dtype)
+    o, S = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    _compare(o, S, starts, q, k, v, alpha, beta, S0, 3, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+def test_strided_in_place_and_parts(dtype):
+    dk = dv = 128
+    H, Hk = 4, 2
+    rng = np.random.default_rng(5)
+    starts, q, k, v, alpha, beta, S0 = _make(rng, [200, 77, 0, 1], H, Hk, dk, dv, dtype)
+    o, S = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    N = v.shape[0]
+    buf = torch.cat([v.flatten(1), torch.full((N, 8), 9.0, dtype=dtype, device="cuda"), k.flatten(1), q.flatten(1)], 1)
+    vs = buf[:, :H * dv].view(N, H, dv)
+    ks = buf[:, H * dv + 8:H * dv + 8 + Hk * dk].view(N, Hk, dk)
+    qs = buf[:, H * dv + 8 + Hk * dk:].view(N, Hk, dk)
+    state = S0.clone()
+    wide = torch.zeros(N, H * dv + 16, dtype=dtype, device="cuda")
+    o2, S2 = _run(starts, qs, ks, vs, alpha, beta, state, dk, dv, S=state, o=wide[:, :H * dv].view(N, H, dv))
+    end = int(starts[-1])
+    assert torch.equal(o2[:end], o[:end]) and torch.equal(state, S) and S2 is state
+    assert not wide[:, H * dv:].any() and not wide[end:].any()
+    # states alone
+    none, S3 = _run(starts, None, k, v, alpha, beta, S0, dk, dv)
+    assert none is None and torch.equal(S3, S)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+def test_prompt_in_parts_continues(dtype):
+    """A prompt cut in two, the second part from the first one's state, is the whole prompt."""
+    dk, dv, H, Hk = 128, 64, 4, 4
+    rng = np.random.default_rng(6)
+    starts, q, k, v, alpha, beta, S0 = _make(rng, [300], H, Hk, dk, dv, dtype, tail=0)
+    _, S1 = _run(np.array([0, 101], np.int32), q[:101], k[:101], v[:101], alpha[:101], beta[:101], S0, dk, dv)
+    o2, S2 = _run(np.array([0, 199], np.int32), q[101:], k[101:], v[101:], alpha[101:].contiguous(),
+                  beta[101:].contiguous(), S1, dk, dv)
+    o, S = _recurrence(list(starts), q, k, v, alpha, beta, S0, 1)
+    om, Sm = _recurrence(list(starts), q.abs(), k.abs(), v.abs(), alpha, beta, S0.abs(), 1)
+    assert ((S2.double() - S).abs() <= 2 * STATE * Sm).all()
+    h = HALF[dtype]
+    tol = (h * (1 + h) + 2 * STATE) * om + max(h, 2.0 ** -24) * o.abs() + 2.0 ** -25
+    assert ((o2.double() - o[101:]).abs() <= tol[101:]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+def test_decays_at_the_ends_of_their_range(dtype):
+    """alpha of 1, 0, next to 0 and next to 1, and beta of 0."""
+    dk, dv, H = 64, 64, 4
+    rng = np.random.default_rng(7)
+    starts, q, k, v, alpha, beta, S0 = _make(rng, [150, 40], H, 2, dk, dv, dtype)
+    alpha[:, 0] = 1.0
+    alpha[:, 1] = 1e-30
+    alpha[::7, 2] = 0.0
+    alpha[:, 3] = 1.0 - 2.0 ** -24
+    beta[::5] = 0.0
+    o, S = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    _compare(o, S, starts, q, k, v, alpha, beta, S0, 2, dtype)
+    alpha[:] = 0.0
+    o, S = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    _compare(o, S, starts, q, k, v, alpha, beta, S0, 2, dtype)
+
+
+@pytest.mark.parametrize("std", [1e-6, 1e-3, 1e3, 3e4])
+def test_scales_of_fp16_values(std):
+    """fp16 activations whose states and scores leave fp16's range, or sink into its subnormals."""
+    dk, dv, H = 128, 64, 2
+    rng = np.random.default_rng(8)
+    starts, q, k, v, alpha, beta, S0 = _make(rng, [200, 33], H, 1, dk, dv, F16, std=1.0)
+    v = (v * min(std, 3e3)).clamp(-6e4, 6e4)
+    S0 = S0 * std
+    q = q * (64.0 if std > 1 else 1.0)   # small: q k and v themselves stay normal numbers where they can
+    k = k * (64.0 if std > 1 else 1.0)
+    q = q * (1.0 / 64 if std > 1e3 else 1.0)
+    o, S = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    ro, rS = _recurrence(list(starts), q, k, v, alpha, beta, S0, 2)
+    om, Sm = _recurrence(list(starts), q.abs(), k.abs(), v.abs(), alpha, beta, S0.abs(), 2)
+    assert ((S.double() - rS).abs() <= STATE * Sm).all()
+    end = int(starts[-1])
+    inside = ro.abs()[:end] < 6e4
+    tol = (HALF[F16] * (1 + HALF[F16]) + STATE) * om + HALF[F16] * ro.abs() + 2.0 ** -25
+    err = (o.double() - ro).abs()[:end]
+    assert (err <= tol[:end])[inside].all()
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+def test_bad_values_stay_in_their_prompt(dtype):
+    """NaN and infinities in one prompt, and in rows of no prompt, leave the others alone."""
+    dk, dv, H = 128, 128, 2
+    rng = np.random.default_rng(9)
+    starts, q, k, v, alpha, beta, S0 = _make(rng, [70, 30, 90], H, 2, dk, dv, dtype, tail=70)
+    good = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    for x in (q, k, v, alpha, beta):
+        x[70:100] = float("nan")
+        x[190:] = float("inf")
+    o, S = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    assert torch.equal(o[:70], good[0][:70]) and torch.equal(o[100:190], good[0][100:190])
+    assert torch.equal(S[[0, 2]], good[1][[0, 2]])
+    assert torch.isnan(S[1]).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+def test_bounds_are_clamped(dtype):
+    dk, dv, H = 64, 64, 2
+    rng = np.random.default_rng(10)
+    starts, q, k, v, alpha, beta, S0 = _make(rng, [80, 60], H, 2, dk, dv, dtype, tail=0)
+    odd = np.array([-5, 80, 2 ** 31 - 1], np.int32)   # as 0, 80, 140
+    a = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    b = _run(odd, q, k, v, alpha, beta, S0, dk, dv)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    back = np.array([100, 20, -4], np.int32)          # falling bounds: both prompts empty
+    o = torch.full_like(v, 3.0)
+    _, S = _run(back, q, k, v, alpha, beta, S0, dk, dv, o=o)
+    assert (o == 3.0).all() and torch.equal(S, S0)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+@pytest.mark.parametrize("lens,H,decay", [([5000], 2, (0.9, 1.0)), ([4097, 0, 900], 1, (0.999, 1.0)), ([2500], 3, (1.0, 1.0)),
+                                          ([30000], 1, (0.9999, 1.0))])
+def test_long_prompts(lens, H, decay, dtype):
+    """Prompts that few heads leave to few CTAs: the long axis is split."""
+    dk, dv = 128, 128
+    rng = np.random.default_rng(11)
+    starts, q, k, v, alpha, beta, S0 = _make(rng, lens, H, 1, dk, dv, dtype, decay=decay)
+    o, S = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    _compare(o, S, starts, q, k, v, alpha, beta, S0, H, dtype)
+    o2, S2 = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    assert torch.equal(o[:int(starts[-1])], o2[:int(starts[-1])]) and torch.equal(S, S2)  # no order but one
+
+
+def test_no_tokens_and_no_prompts():
+    dk, dv, H = 64, 32, 2
+    rng = np.random.default_rng(12)
+    starts, q, k, v, alpha, beta, S0 = _make(rng, [0, 0], H, 2, dk, dv, BF16, tail=0)
+    o, S = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    assert o.shape == (0, H, dv) and torch.equal(S, S0)
+    o, S = _run(starts, q, k, v, alpha, beta, None, dk, dv)
+    assert not S.any()
+    o, S = _run(starts[:1], q, k, v, alpha, beta, None, dk, dv)
+    assert S.shape == (0, H, dv, dk)
+    torch.cuda.synchronize()
+
+
+def test_captured_and_on_other_streams():
+    from ssm_decode_step_b200 import PackedPrefill
+    dk, dv, H = 128, 64, 8
+    rng = np.random.default_rng(13)
+    starts, q, k, v, alpha, beta, S0 = _make(rng, [130, 700, 64], H, 2, dk, dv, BF16, tail=30)
+    plan = PackedPrefill(_cfg(dk, dv), H, 2, max_tokens=2000, max_sequences=5)
+    st = torch.from_numpy(starts).cuda()
+    o, S = torch.zeros_like(v), torch.zeros_like(S0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        plan.run(st, q, k, v, alpha, beta, S0=S0, S=S, o=o)
+    torch.cuda.current_stream().wait_stream(side)
+    want = o.clone(), S.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        plan.run(st, q, k, v, alpha, beta, S0=S0, S=S, o=o)
+    o.zero_()
+    S.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(S, want[1])
+    # other bounds in the captured arrays
+    other = np.array([0, 300, 300, 924], np.int32)
+    st.copy_(torch.from_numpy(other))
+    g.replay()
+    o2, S2 = plan.run(st, q, k, v, alpha, beta, S0=S0, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(o2[:924], o[:924]) and torch.equal(S2, S)
+    _compare(o, S, other, q, k, v, alpha, beta, S0, 4, BF16)
+
+
+def test_serving_loop():
+    """Prompts into slots, tokens from them, and a prompt taken up again from its quantized state: the
+    operators as a serving program runs them, each against 64 bits on what it was given."""
+    from ssm_decode_step_b200 import Config, PackedPrefill, StateCache
+    dk, dv, H, Hk, pool = 128, 64, 4, 2, 6
+    rng = np.random.default_rng(14)
+    cfg = Config(pool * H, dk, dv, 8, 32, 0, "scalar", "dynamic")
+    cache = StateCache(cfg, H)
+    plan = PackedPrefill(cfg, H, Hk, max_tokens=1000, max_sequences=4)
+    lens = [120, 33, 300]
+    starts, q, k, v, alpha, beta, _ = _make(rng, lens, H, Hk, dk, dv, BF16)
+    o, S = plan.run(torch.from_numpy(starts).cuda(), q, k, v, alpha, beta)
+    _compare(o, S, starts, q, k, v, alpha, beta, None, 2, BF16)
+    slots = torch.tensor([4, 1, 5], dtype=torch.int32, device="cuda")
+    cache.write(slots, S)
+    kept = cache.read(slots).double()
+    step = S.double().unflatten(-1, (-1, 32)).abs().amax(-1, keepdim=True).expand(-1, -1, -1, -1, 32).flatten(-2) / 127
+    assert ((kept - S.double()).abs() <= step * 0.5001).all()
+    for t in range(4):
+        s1, q1, k1, v1, a1, b1, _ = _make(rng, [1, 1, 1], H, Hk, dk, dv, BF16, tail=0)
+        o1 = cache.step(slots, q1, k1, v1, a1, b1)
+        ro, rS = _recurrence([0, 1, 2, 3], q1, k1, v1, a1, b1, kept, 2)
+        om, _ = _recurrence([0, 1, 2, 3], q1.abs(), k1.abs(), v1.abs(), a1, b1, kept.abs(), 2)
+        assert ((o1.double() - ro).abs() <= 2.0 ** -18 * om + 2.0 ** -8 * ro.abs()).all()
+        kept = cache.read(slots).double()
+        group = rS.unflatten(-1, (-1, 32)).abs().amax(-1, keepdim=True).expand(-1, -1, -1, -1, 32).flatten(-2)
+        assert ((kept - rS).abs() <= group / 127 * 0.5001).all()
+    # the second prompt goes on from its slot
+    more, q, k, v, alpha, beta, _ = _make(rng, [90], H, Hk, dk, dv, BF16)
+    S0 = cache.read(slots[1:2])
+    o, S = plan.run(torch.from_numpy(more).cuda(), q, k, v, alpha, beta, S0=S0)
+    _compare(o, S, more, q, k, v, alpha, beta, S0, 2, BF16)
+    others = cache.codes[[4, 5]].clone()
+    cache.write(slots[1:2], S)
+    assert torch.equal(cache.codes[[4, 5]], others)
