@@ -476,8 +476,8 @@ QS_API qs_status qstate_cache_step(const qs_config* cfg, const qs_tokens* batch,
  * activations to about 2^-16 of the magnitudes summed; the operands of the
  * outputs (the decayed scores, and the state where it is read) are rounded
  * to dtype once.  FP32 activations run on the CUDA cores in FP32.
- * A decay of exactly 0 forgets everything before its token; a decay below
- * 2^-120 counts as 0.
+ * A decay of 0 forgets everything before its token; with 16-bit activations
+ * a decay below 2^-120 counts as 0.
  *
  * workspace: device memory of at least qstate_prefill_packed_workspace bytes
  * (which depends on the batch's sizes alone, and grows with tokens and
@@ -491,6 +491,11 @@ QS_API qs_status qstate_prefill_packed(const qs_config* cfg, const qs_tokens* ba
                                        const void* q, const void* k, const void* v,
                                        const float* alpha, const float* beta, void* o,
                                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Number of CTAs of qstate_prefill_packed whose bounded wait gave up since
+ * the library was loaded (current device; synchronous); 0 unless the device
+ * is in trouble.  o and S1 of a launch that raised it are undefined. */
+QS_API qs_status qstate_prefill_packed_timeouts(unsigned int* count);
 
 /* Squared Frobenius norm of every tile of the stored state, for tracking
  * the state norm over a decode horizon (the norm inflation of per-token

@@ -1,59 +1,19 @@
-// C entry points of the state cache and of the packed prefill
-// (include/qstate.h): argument checks and dispatch.  No memory is allocated.
-#include <climits>
+// C entry points of the state cache (include/qstate.h): argument checks and
+// dispatch.  No memory is allocated.
 
 #include "qstate_cache.cuh"
 #include "qstate_check.h"
 #include "qstate_launch.h"
-#include "qstate_packed.cuh"
 
 namespace {
 
 using namespace qs;
-
-bool valid_dtype(int d) { return d == QS_F32 || d == QS_F16 || d == QS_BF16; }
 
 // The pool: the family's fields, heads that divide its tiles.
 qs_status check_pool(const qs_config* c, int heads) {
   const qs_status st = check_config(c);
   if (st != QS_OK) return st;
   if (heads < 1 || c->num_tiles % heads != 0) return QS_ERR_INVALID_ARG;
-  return QS_OK;
-}
-
-// A batch's tiles fit 32-bit row block counts (row blocks of 8 or 16 rows).
-bool batch_fits(const qs_config* c, long long entries, long long heads) {
-  return entries * heads * (c->dv / 8) <= 0x7fffffffLL;
-}
-
-struct TokenRanges {
-  Range q, k, v, o;
-};
-
-// The layout of q, k, v, o in `b`, and the pointers' alignment.
-qs_status check_tokens(const qs_config* c, const qs_tokens* b, const void* q, const void* k, const void* v,
-                       const void* o, TokenRanges* r) {
-  const size_t e = dtype_bytes(b->dtype);
-  const size_t qk = static_cast<size_t>(b->qk_heads) * c->dk, vo = static_cast<size_t>(b->heads) * c->dv;
-  const int64_t strides[4] = {b->q_stride, b->k_stride, b->v_stride, b->o_stride};
-  const size_t width[4] = {qk, qk, vo, vo};
-  const void* ptr[4] = {q, k, v, o};
-  Range out[4];
-  for (int i = 0; i < 4; ++i) {
-    out[i] = range_of(nullptr, 0);
-    if (ptr[i] == nullptr) continue;
-    if (strides[i] < static_cast<int64_t>(width[i]) || strides[i] > (1LL << 40)) return QS_ERR_INVALID_ARG;
-    if ((static_cast<size_t>(strides[i]) * e) % 16 != 0 || !aligned(ptr[i], 16)) return QS_ERR_INVALID_ARG;
-    out[i] = range_of(ptr[i], (static_cast<size_t>(b->tokens - 1) * strides[i] + width[i]) * e);
-  }
-  *r = {out[0], out[1], out[2], out[3]};
-  return QS_OK;
-}
-
-qs_status check_batch(const qs_tokens* b) {
-  if (b == nullptr || b->tokens < 0 || b->heads < 1 || b->qk_heads < 1 || b->heads % b->qk_heads != 0 ||
-      !valid_dtype(b->dtype))
-    return QS_ERR_INVALID_ARG;
   return QS_OK;
 }
 
@@ -130,34 +90,6 @@ cudaError_t dispatch_cache_step(const qs_config* c, const StreamParams& p, int t
   }
 }
 
-// The recurrence's fields of cfg, the packed batch and the number of prompts.
-qs_status check_packed(const qs_config* cfg, const qs_tokens* b, int sequences, qs_config* out) {
-  if (cfg == nullptr) return QS_ERR_INVALID_ARG;
-  qs_config c = *cfg;  // storage fields do not matter here
-  c.num_tiles = 0;
-  c.bits = 8;
-  c.group = 32;
-  c.policy = QS_SCALE_PERSISTENT;
-  c.rounding = QS_ROUND_NEAREST;
-  qs_status st = check_config(&c);
-  if (st != QS_OK) return st;
-  st = check_batch(b);
-  if (st != QS_OK) return st;
-  if (sequences < 0) return QS_ERR_INVALID_ARG;
-  if (c.delta != 0 || c.decay != QS_DECAY_SCALAR) return QS_ERR_UNSUPPORTED;
-  if (!batch_fits(&c, sequences, b->heads)) return QS_ERR_UNSUPPORTED;
-  *out = c;
-  return QS_OK;
-}
-
-template <int DK, class E>
-cudaError_t launch_recurrent(PackedParams p, int sequences, cudaStream_t stream) {
-  constexpr int ROWS = kPackThreads / (DK / 16);
-  p.blocks = (p.dv + ROWS - 1) / ROWS;
-  packed_recurrent_kernel<DK, E><<<static_cast<unsigned>(sequences) * p.heads * p.blocks, kPackThreads, 0, stream>>>(p);
-  return cudaGetLastError();
-}
-
 }  // namespace
 
 extern "C" {
@@ -221,71 +153,6 @@ qs_status qstate_cache_step(const qs_config* cfg, const qs_tokens* batch, const 
     e = cfg->dk == 64 ? dispatch_cache_step<4, 64>(cfg, p, n, stream) : dispatch_cache_step<4, 128>(cfg, p, n, stream);
   else
     e = cfg->dk == 64 ? dispatch_cache_step<8, 64>(cfg, p, n, stream) : dispatch_cache_step<8, 128>(cfg, p, n, stream);
-  return from_cuda(e);
-}
-
-qs_status qstate_prefill_packed_workspace(const qs_config* cfg, const qs_tokens* batch, int sequences,
-                                          size_t* bytes) {
-  qs_config c;
-  const qs_status st = check_packed(cfg, batch, sequences, &c);
-  if (st != QS_OK) return st;
-  if (bytes) *bytes = 0;
-  return QS_OK;
-}
-
-qs_status qstate_prefill_packed(const qs_config* cfg, const qs_tokens* batch, int sequences, const int32_t* starts,
-                                const float* S0, float* S1, const void* q, const void* k, const void* v,
-                                const float* alpha, const float* beta, void* o, void* workspace,
-                                size_t workspace_bytes, cudaStream_t stream) {
-  qs_config c;
-  qs_status st = check_packed(cfg, batch, sequences, &c);
-  if (st != QS_OK) return st;
-  if (sequences == 0) return QS_OK;
-  const bool any = batch->tokens > 0;
-  if (!starts || !S1 || (any && (!k || !v || !alpha || !beta || (o && !q)))) return QS_ERR_INVALID_ARG;
-  if (!aligned(starts, 4) || !aligned(S1, 16) || (S0 && !aligned(S0, 16)) || !aligned(alpha, 4) || !aligned(beta, 4))
-    return QS_ERR_INVALID_ARG;
-  TokenRanges t = {};
-  if (any) {
-    st = check_tokens(&c, batch, q, k, v, o, &t);
-    if (st != QS_OK) return st;
-  }
-  size_t need = 0;
-  qstate_prefill_packed_workspace(cfg, batch, sequences, &need);
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return QS_ERR_INVALID_ARG;
-  const size_t tiles = static_cast<size_t>(sequences) * batch->heads;
-  const size_t state = tiles * c.dv * c.dk * sizeof(float);
-  const size_t gates = any ? static_cast<size_t>(batch->tokens) * batch->heads * sizeof(float) : 0;
-  const Range w[3] = {range_of(S1, state), t.o, range_of(need ? workspace : nullptr, need)};
-  const Range r[7] = {t.q, t.k, t.v, range_of(alpha, gates), range_of(beta, gates),
-                      range_of(starts, (static_cast<size_t>(sequences) + 1) * 4),
-                      range_of(S0 == S1 ? nullptr : S0, S0 && S0 != S1 ? state : 0)};
-  if (any_overlap(w, 3, r, 7)) return QS_ERR_INVALID_ARG;
-  PackedParams p;
-  p.starts = starts;
-  p.S0 = S0;
-  p.S1 = S1;
-  p.q = q;
-  p.k = k;
-  p.v = v;
-  p.alpha = alpha;
-  p.beta = beta;
-  p.o = o;
-  p.q_stride = batch->q_stride;
-  p.k_stride = batch->k_stride;
-  p.v_stride = batch->v_stride;
-  p.o_stride = batch->o_stride;
-  p.tokens = batch->tokens;
-  p.heads = batch->heads;
-  p.share = batch->heads / batch->qk_heads;
-  p.dv = c.dv;
-  p.blocks = 0;
-  cudaError_t e;
-#define QS_REC(DK) (batch->dtype == QS_F32 ? launch_recurrent<DK, F32>(p, sequences, stream) \
-                    : batch->dtype == QS_F16 ? launch_recurrent<DK, F16>(p, sequences, stream) \
-                                             : launch_recurrent<DK, BF16>(p, sequences, stream))
-  e = c.dk == 64 ? QS_REC(64) : QS_REC(128);
-#undef QS_REC
   return from_cuda(e);
 }
 

@@ -72,4 +72,44 @@ inline bool any_overlap(const Range* written, int nw, const Range* read, int nr)
   return false;
 }
 
+inline size_t dtype_bytes(int dtype) { return dtype == QS_F32 ? 4 : 2; }
+
+inline bool valid_dtype(int d) { return d == QS_F32 || d == QS_F16 || d == QS_BF16; }
+
+// A batch's tiles fit 32-bit row block counts (row blocks of 8 or 16 rows).
+inline bool batch_fits(const qs_config* c, long long entries, long long heads) {
+  return entries * heads * (c->dv / 8) <= 0x7fffffffLL;
+}
+
+struct TokenRanges {
+  Range q, k, v, o;
+};
+
+// The layout of q, k, v, o in `b`, and the pointers' alignment.
+inline qs_status check_tokens(const qs_config* c, const qs_tokens* b, const void* q, const void* k, const void* v,
+                       const void* o, TokenRanges* r) {
+  const size_t e = dtype_bytes(b->dtype);
+  const size_t qk = static_cast<size_t>(b->qk_heads) * c->dk, vo = static_cast<size_t>(b->heads) * c->dv;
+  const int64_t strides[4] = {b->q_stride, b->k_stride, b->v_stride, b->o_stride};
+  const size_t width[4] = {qk, qk, vo, vo};
+  const void* ptr[4] = {q, k, v, o};
+  Range out[4];
+  for (int i = 0; i < 4; ++i) {
+    out[i] = range_of(nullptr, 0);
+    if (ptr[i] == nullptr) continue;
+    if (strides[i] < static_cast<int64_t>(width[i]) || strides[i] > (1LL << 40)) return QS_ERR_INVALID_ARG;
+    if ((static_cast<size_t>(strides[i]) * e) % 16 != 0 || !aligned(ptr[i], 16)) return QS_ERR_INVALID_ARG;
+    out[i] = range_of(ptr[i], (static_cast<size_t>(b->tokens - 1) * strides[i] + width[i]) * e);
+  }
+  *r = {out[0], out[1], out[2], out[3]};
+  return QS_OK;
+}
+
+inline qs_status check_batch(const qs_tokens* b) {
+  if (b == nullptr || b->tokens < 0 || b->heads < 1 || b->qk_heads < 1 || b->heads % b->qk_heads != 0 ||
+      !valid_dtype(b->dtype))
+    return QS_ERR_INVALID_ARG;
+  return QS_OK;
+}
+
 }  // namespace qs

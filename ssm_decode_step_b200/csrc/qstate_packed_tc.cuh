@@ -1,0 +1,828 @@
+// Prefill of packed prompts on the tensor cores (qstate_prefill_packed, 16-bit
+// activations): linear attention with a decay for each head, in chunks of 64
+// tokens.
+//
+// Mathematics.  Within a chunk, with G_t the running log2-decay (inclusive)
+// and C its last token, S the state before it,
+//   o_t    = 2^{G_t} S q_t + sum_{s<=t} (q_t . k_s) 2^{G_t - G_s} beta_s v_s
+//   S_out  = 2^{G_C} S + sum_s (2^{G_C - G_s} beta_s v_s) k_s^T
+// Only differences G_t - G_s with s <= t are exponentiated, so nothing
+// overflows.  G is summed in FP64 and kept as an integer and a fraction, each
+// exact enough in FP32 that a difference of neighbours far down a chunk is off
+// by 2^-23, whatever the decays before them.  A decay below 2^-120 is a
+// reset: it leaves the running sum alone and cuts the tokens before it off.
+//
+// One CTA per SM works on (prompt, head, block of MDV rows of S) items, one
+// after the other, with the chunks of all its items in one pipeline.  Four
+// contractions per chunk, tcgen05.mma with FP32 accumulators in tensor
+// memory (columns in brackets):
+//   scores  [64 x 64]   q k^T                      q, k from shared memory
+//   KV      [MDV x Dk]  W k                        W from tensor memory
+//   O1      [MDV x 64]  S q^T                      S from tensor memory
+//   O2      [MDV x 64]  v^T P^T                    v, P from shared memory
+// with W[i][s] = 2^{G_C - G_s} beta_s v_s[i] and P[t][s] the masked, decayed
+// scores.  Outputs are transposed (a lane per row of S, a column per token),
+// which lets the chunk stay at 64 tokens with all 128 lanes in use.
+//
+// Precision.  The state lives in FP32 registers, updated by one fused
+// multiply-add per chunk, so nothing accumulates in the tensor core beyond a
+// chunk.  W is split into two 16-bit parts (the value and its rounding
+// error), which keeps 2^-16 (bf16) of every term of the state; P, and S
+// where O1 reads it, are rounded once to the activations' type, as the
+// outputs are; the factor 2^{G_t} is applied to O1 in FP32.  fp16 has a
+// narrow range: W, S and P are scaled there by a power of two for each of
+// their rows, taken out again in FP32.
+//
+// Warps: 0 loads q, k, v by TMA (128-byte swizzle, a ring of stages); 1
+// issues the contractions; 2 turns alpha and beta into the chunk's factors; 3
+// holds the tensor memory; 4-7 form P from the scores and write the outputs;
+// 8-15 form W and own the state (each of the two warpgroups half of W's
+// tokens and half of S's columns).  All hand-offs are mbarriers; every wait
+// is bounded, and on a timeout the CTA counts it, waits for its copies,
+// frees its tensor memory and returns.
+#pragma once
+
+#include <cuda.h>
+
+#include "qstate_packed.cuh"
+#include "qstate_prefill_tc.cuh"
+
+namespace qs {
+
+constexpr int kPtThreads = 512;
+constexpr int kPtChunk = 64;
+// tensor-memory columns
+constexpr uint32_t kPtColScore = 0, kPtColO1 = 64, kPtColO2 = 128, kPtColKV = 192, kPtColS = 320, kPtColW = 384;
+constexpr float kPtReset = 0x1p-120f;
+
+struct PackedTcParams {
+  PackedParams p;
+  int items;  // prompts * heads * row blocks
+};
+
+// Shared memory of a CTA (byte offsets from a 1024-byte boundary).
+template <int DK, int MDV>
+struct PtLayout {
+  static constexpr int kPanel = kPtChunk * 128;  // 64 tokens x 64 columns, 128-byte swizzled
+  static constexpr int kQ = 0, kK = DK / 64 * kPanel, kV = 2 * kK, kStage = kV + MDV / 64 * kPanel;
+  static constexpr int kStages = DK == 128 ? 4 : 5;
+  static constexpr int kP = kStages * kStage;           // two buffers of 64 x 64
+  static constexpr int kGate = kP + 2 * kPanel;         // per stage, see Gate
+  static constexpr int kGateSlot = 6 * 256 + 128;
+  static constexpr int kScaleS = kGate + kStages * kGateSlot;  // fp16: 2 x 128 row scales of S
+  static constexpr int kScaleP = kScaleS + 1024;               // fp16: 2 x 64 row scales of P
+  static constexpr int kMax = kScaleP + 512;                   // fp16: 4 x 2 x 128 row maxima
+  static constexpr int kBars = kMax + 4096;
+  static constexpr int kBytes = kBars + 320 + 1024;
+};
+
+// A chunk's factors, in floats from its gate slot: the integers and
+// fractions of G, beta, W's weights 2^{G_C - G} beta, 2^G, the first token
+// that a token still sees (int), and 2^{G_C}.
+struct Gate {
+  static constexpr int kInt = 0, kFrac = 64, kBeta = 128, kW = 192, kDecay = 256, kFirst = 320, kLast = 384;
+};
+
+// mbarriers, 8 bytes each
+template <int NST>
+struct PtBars {
+  static constexpr int kFull = 0, kEmpty = NST, kGateFull = 2 * NST, kGateFree = 3 * NST, kScFull = 4 * NST,
+                       kScFree = kScFull + 1, kPFull = kScFull + 2, kPFree = kPFull + 2, kWFull = kPFree + 2,
+                       kKvFull = kWFull + 2, kKvFree = kKvFull + 1, kSFull = kKvFree + 1, kO1Done = kSFull + 1,
+                       kOFull = kO1Done + 1, kOFree = kOFull + 1, kPair = kOFree + 1, kCount = kPair + 1;
+};
+
+namespace pt {
+
+using namespace tc;
+
+// Instruction descriptor: FP32 accumulator, 16-bit A and B; `at`, `bt`: the
+// operand's rows (M or N) are contiguous in shared memory instead of K.
+template <class E>
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool at, bool bt) {
+  constexpr uint32_t f = E::kTag == QS_BF16 ? 1u : 0u;
+  return (1u << 4) | (f << 7) | (f << 10) | (at ? 1u << 15 : 0u) | (bt ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Shared-memory descriptor of a 128-byte swizzled operand whose 8-row groups
+// lie 1024 bytes apart; `lbo`: distance of the next 64 contiguous elements
+// (operands whose rows are contiguous).
+__device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lbo) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+         static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
+// One look at the phase of the given parity.
+__device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// The wait proper, out of line: false once it, or another wait of the CTA
+// (`failed`), gave up.
+static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* failed) {
+  for (int round = 0; round < 256; ++round) {
+    for (int i = 0; i < 1024; ++i)
+      if (mbar_done(bar, parity)) return true;
+    if (*failed) return false;
+  }
+  *failed = 1;
+  return false;
+}
+
+__device__ __forceinline__ void mma16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+          "r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// 16 lanes x 64 columns over all 32 threads: registers 4j .. 4j+3 are row
+// T/4 (two columns 8j + 2 (T%4)) and row T/4 + 8 (the same columns).
+__device__ __forceinline__ void tm_ld_16x64(uint32_t addr, float (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tm_st16u(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tm_st8u(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The power of two that brings a row whose largest magnitude is m into
+// [2^13, 2^14) (1 for a row of zeros, infinities or NaN); its inverse in
+// `back`.  Both are normal numbers.
+__device__ __forceinline__ float row_scale(float m, float& back) {
+  const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+  const int up = m > 0.0f && e < 128 ? min(max(13 - e, -120), 120) : 0;
+  back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+}
+
+}  // namespace pt
+
+// CTAs whose wait gave up since the library was loaded.
+static __device__ unsigned int packed_timeouts = 0;
+
+template <class E, int DK, int MDV>
+__global__ void __launch_bounds__(kPtThreads, 1)
+    packed_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, const PackedTcParams a) {
+  using namespace pt;
+  using L = PtLayout<DK, MDV>;
+  constexpr int NST = L::kStages;
+  using B = PtBars<NST>;
+  static_assert(B::kCount * 8 + 8 <= 320, "barriers fit their space");
+  constexpr int C = kPtChunk;
+  constexpr bool HALF = E::kTag == QS_F16;
+  using T = typename E::T;
+  extern __shared__ unsigned char raw[];
+  const PackedParams& p = a.p;
+  const uint32_t base = (saddr(raw) + 1023u) & ~1023u;
+  unsigned char* const sm = raw + (base - saddr(raw));
+  uint32_t* const tslot = reinterpret_cast<uint32_t*>(sm + L::kBars + 8 * B::kCount);
+  volatile uint32_t* const failed = tslot + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int qd = warp & 3;
+  const bool outputs = p.o != nullptr;
+  auto bar = [&](int i) { return base + L::kBars + 8 * i; };
+
+  if (warp == 3) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tslot)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int s = 0; s < NST; ++s) {
+      bar_init(bar(B::kFull + s), 1);
+      bar_init(bar(B::kEmpty + s), 1 + 8);                   // the contractions; W's warps
+      bar_init(bar(B::kGateFull + s), 1);
+      bar_init(bar(B::kGateFree + s), outputs ? 4 + 8 : 8);  // its readers
+    }
+    bar_init(bar(B::kScFull), 1);
+    bar_init(bar(B::kScFree), 4);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bar(B::kPFull + i), 4);
+      bar_init(bar(B::kPFree + i), 1);
+      bar_init(bar(B::kWFull + i), 8);
+    }
+    bar_init(bar(B::kKvFull), 1);
+    bar_init(bar(B::kKvFree), 8);
+    bar_init(bar(B::kSFull), 8);
+    bar_init(bar(B::kO1Done), 1);
+    bar_init(bar(B::kOFull), 1);
+    bar_init(bar(B::kOFree), 4);
+    bar_init(bar(B::kPair), 8);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    *failed = 0;
+  }
+  // P above the diagonal blocks stays zero
+  for (int i = tid; i < 2 * L::kPanel / 16; i += kPtThreads)
+    *reinterpret_cast<uint4*>(sm + L::kP + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+  fence_async_smem();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  // all columns are this CTA's, so the allocation starts at column 0
+  constexpr uint32_t tm = 0;
+  const uint32_t tw = tm + (static_cast<uint32_t>(32 * qd) << 16);  // this warp's lanes
+
+  // Wait for completion number n of a barrier (the caller's count; n < 0:
+  // nothing to wait for).  False once this wait or another gave up.
+  // `wait` is for one thread, `wait_all` for a whole warp.
+  auto wait = [&](int b, int n) -> bool {
+    const uint32_t addr = bar(b), parity = static_cast<uint32_t>(n) & 1u;
+    return n < 0 || mbar_done(addr, parity) || mbar_wait_long(addr, parity, failed);
+  };
+  auto wait_all = [&](int b, int n) -> bool {
+    if (n < 0) return true;
+    const uint32_t addr = bar(b), parity = static_cast<uint32_t>(n) & 1u;
+    if (__all_sync(0xffffffffu, mbar_done(addr, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait_long(addr, parity, failed));
+  };
+  // The warp's work so far is visible to whoever waits for this arrival.
+  auto signal = [&](int b) {
+    __syncwarp();
+    if (lane == 0) arrive(bar(b));
+  };
+
+  struct Item {
+    int tile, head, blk, begin, end, chunks;
+  };
+  auto item_at = [&](int it) {
+    Item x;
+    x.blk = it % p.blocks;
+    x.tile = it / p.blocks;
+    const int seq = x.tile / p.heads;
+    x.head = x.tile - seq * p.heads;
+    prompt_bounds(p.starts, seq, p.tokens, x.begin, x.end);
+    x.chunks = (x.end - x.begin + C - 1) / C;
+    return x;
+  };
+  const int irow = tc_row<MDV>(qd, lane);  // row of W, S and the outputs of this lane
+
+  bool ok = true;
+  int g = 0;  // chunks so far, over all items of this CTA
+  if (warp == 0) {
+    // ---- loads
+    if (lane == 0) {
+      for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+        const Item x = item_at(it);
+        for (int c = 0; ok && c < x.chunks; ++c, ++g) {
+          const int st = g % NST;
+          if (!(ok = wait(B::kEmpty + st, g / NST - 1))) break;
+          const uint32_t s = base + st * L::kStage, f = bar(B::kFull + st);
+          expect_tx(f, (outputs ? L::kStage : L::kStage - L::kK));
+          const int t = x.begin + c * C;
+          for (int i = 0; i < DK / 64; ++i) {
+            if (outputs) tma_load3(s + L::kQ + i * L::kPanel, &mq, 64 * i, x.head / p.share, t, f);
+            tma_load3(s + L::kK + i * L::kPanel, &mk, 64 * i, x.head / p.share, t, f);
+          }
+          for (int i = 0; i < MDV / 64; ++i)
+            tma_load3(s + L::kV + i * L::kPanel, &mv, x.blk * MDV + 64 * i, x.head, t, f);
+        }
+      }
+      // after a timeout: the copies in flight land before the CTA leaves
+      if (!ok)
+        for (int j = max(0, g - NST); j < g; ++j) mbar_wait(bar(B::kFull + j % NST), (j / NST) & 1, 1 << 16);
+    }
+  } else if (warp == 1) {
+    // ---- contractions: KV(g), O1(g), scores(g + 1), O2(g).  The whole warp
+    // runs the loop, so that addresses stay uniform; one lane issues.
+    constexpr uint32_t id_sc = idesc<E>(C, C, false, false), id_kv = idesc<E>(MDV, DK, false, true),
+                       id_o1 = idesc<E>(MDV, C, false, false), id_o2 = idesc<E>(MDV, C, true, false);
+    // descriptors of stage 0; a byte offset adds a sixteenth of itself
+    const uint64_t dq = desc128(base + L::kQ, 16), dk = desc128(base + L::kK, 16),
+                   dkt = desc128(base + L::kK, L::kPanel), dv = desc128(base + L::kV, L::kPanel),
+                   dp = desc128(base + L::kP, 16);
+    const bool lead = elect_one();
+    auto scores = [&](int n) -> bool {
+      const uint32_t s = (n % NST) * (L::kStage / 16);
+      if (!wait_all(B::kFull + n % NST, n / NST) || !wait_all(B::kScFree, n - 1)) return false;
+      fence_after();
+      if (lead) {
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k) {
+          const uint32_t off = s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16;
+          mma16_ss(tm + kPtColScore, dq + off, dk + off, id_sc, k > 0);
+        }
+        mma_commit(bar(B::kScFull));
+      }
+      return true;
+    };
+    int total = 0;
+    for (int it = blockIdx.x; it < a.items; it += gridDim.x) total += item_at(it).chunks;
+    if (outputs && total > 0) ok = scores(0);
+#pragma unroll 1
+    for (; ok && g < total; ++g) {
+      const int st = g % NST;
+      const uint32_t s = st * (L::kStage / 16);
+      if (!(ok = wait_all(B::kFull + st, g / NST) && wait_all(B::kWFull + (g & 1), g >> 1) && wait_all(B::kKvFree, g - 1)))
+        break;
+      fence_after();
+      if (lead) {
+        const uint32_t w = tm + kPtColW + 64 * (g & 1);
+#pragma unroll
+        for (int k = 0; k < C / 8; ++k)  // 4 steps of W's value, 4 of its rounding error
+          mma16_ts(tm + kPtColKV, w + 8 * k, dkt + (s + (k % 4) * (2048 / 16)), id_kv, k > 0);
+        mma_commit(bar(B::kKvFull));
+      }
+      if (outputs) {
+        if (!(ok = wait_all(B::kSFull, g) && wait_all(B::kOFree, g - 1))) break;
+        fence_after();
+        if (lead) {
+#pragma unroll
+          for (int k = 0; k < DK / 16; ++k)
+            mma16_ts(tm + kPtColO1, tm + kPtColS + 8 * k, dq + (s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16), id_o1,
+                     k > 0);
+          mma_commit(bar(B::kO1Done));
+        }
+        if (g + 1 < total && !(ok = scores(g + 1))) break;
+        if (!(ok = wait_all(B::kPFull + (g & 1), g >> 1))) break;
+        fence_after();
+        if (lead) {
+          const uint32_t pb = (g & 1) * (L::kPanel / 16);
+#pragma unroll
+          for (int k = 0; k < C / 16; ++k)
+            mma16_ss(tm + kPtColO2, dv + (s + k * (2048 / 16)), dp + (pb + 2 * k), id_o2, k > 0);
+          mma_commit(bar(B::kOFull));
+          mma_commit(bar(B::kPFree + (g & 1)));
+        }
+      }
+      if (lead) mma_commit(bar(B::kEmpty + st));
+      __syncwarp();
+    }
+  } else if (warp == 2) {
+    // ---- the chunk's factors from alpha and beta, one chunk's loads ahead
+    int it = blockIdx.x, c = 0;
+    Item x{};
+    float a0, a1, b0, b1;
+    auto seek = [&]() {  // the first item from `it` on that has chunks
+      while (it < a.items) {
+        x = item_at(it);
+        if (x.chunks > 0) return;
+        it += gridDim.x;
+      }
+    };
+    auto load = [&]() {
+      const int t = x.begin + c * C, n = x.end - t;
+      const size_t at = static_cast<size_t>(t + lane) * p.heads + x.head, at1 = at + static_cast<size_t>(32) * p.heads;
+      a0 = lane < n ? __ldg(p.alpha + at) : 1.0f;
+      b0 = lane < n ? __ldg(p.beta + at) : 0.0f;
+      a1 = lane + 32 < n ? __ldg(p.alpha + at1) : 1.0f;
+      b1 = lane + 32 < n ? __ldg(p.beta + at1) : 0.0f;
+    };
+    seek();
+    if (it < a.items) load();
+    while (it < a.items) {
+      const int st = g % NST;
+      const float be0 = b0, be1 = b1;
+      const bool z0 = a0 < kPtReset, z1 = a1 < kPtReset;
+      double x0 = z0 ? 0.0 : static_cast<double>(log2f(a0)), x1 = z1 ? 0.0 : static_cast<double>(log2f(a1));
+      if (++c == x.chunks) {
+        c = 0;
+        it += gridDim.x;
+        seek();
+      }
+      if (it < a.items) load();
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const double y0 = __shfl_up_sync(0xffffffffu, x0, d), y1 = __shfl_up_sync(0xffffffffu, x1, d);
+        if (lane >= d) {
+          x0 += y0;
+          x1 += y1;
+        }
+      }
+      x1 += __shfl_sync(0xffffffffu, x0, 31);
+      const double gc = __shfl_sync(0xffffffffu, x1, 31);
+      // the last reset at or before a token: what lies before it is forgotten
+      const uint32_t m0 = __ballot_sync(0xffffffffu, z0), m1 = __ballot_sync(0xffffffffu, z1);
+      const uint32_t le = 0xffffffffu >> (31 - lane);
+      const int r0 = (m0 & le) ? 31 - __clz(m0 & le) : -1;
+      const int r31 = m0 ? 31 - __clz(m0) : -1;
+      const int r1 = (m1 & le) ? 63 - __clz(m1 & le) : r31;
+      const int rc = m1 ? 63 - __clz(m1) : r31;
+      if (!(ok = wait_all(B::kGateFree + st, g / NST - 1))) break;
+      float* f = reinterpret_cast<float*>(sm + L::kGate + st * L::kGateSlot);
+      int* first = reinterpret_cast<int*>(f + Gate::kFirst);
+      auto put = [&](int t, double x, float be, int r) {
+        const double whole = rint(x);
+        f[Gate::kInt + t] = static_cast<float>(whole);
+        f[Gate::kFrac + t] = static_cast<float>(x - whole);
+        f[Gate::kBeta + t] = be;
+        f[Gate::kW + t] = t >= rc ? be * ex2(static_cast<float>(gc - x)) : 0.0f;
+        f[Gate::kDecay + t] = r < 0 ? exp2f(static_cast<float>(x)) : 0.0f;
+        first[t] = max(r, 0);
+      };
+      put(lane, x0, be0, r0);
+      put(lane + 32, x1, be1, r1);
+      if (lane == 0) f[Gate::kLast] = rc < 0 ? exp2f(static_cast<float>(gc)) : 0.0f;
+      signal(B::kGateFull + st);
+      ++g;
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---- P(g + 1), then the outputs of g
+    if (outputs) {
+      auto form_p = [&](int n) -> bool {
+        const int st = n % NST, buf = n & 1;
+        if (!wait_all(B::kGateFull + st, n / NST) || !wait_all(B::kScFull, n)) return false;
+        fence_after();
+        float r[32];
+        tm_ld_16x64(tw + kPtColScore, r);
+        wait_ld();
+        fence_before();
+        signal(B::kScFree);
+        const float* f = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot);
+        const int* first = reinterpret_cast<const int*>(f + Gate::kFirst);
+        const int t0 = 16 * qd + lane / 4, t1 = t0 + 8, cc = 2 * (lane % 4);
+        const float2 i0 = f2(f[Gate::kInt + t0]), i1 = f2(f[Gate::kInt + t1]);
+        const float2 f0 = f2(f[Gate::kFrac + t0]), f1 = f2(f[Gate::kFrac + t1]);
+        const int l0 = first[t0], l1 = first[t1];
+        float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j >= 2 * (qd + 1)) continue;  // above the diagonal: P stays zero there
+          const int s = 8 * j + cc;
+          auto at = [&](int k) { return *reinterpret_cast<const float2*>(f + k + s); };
+          const float2 is = at(Gate::kInt), fs = at(Gate::kFrac), be = at(Gate::kBeta);
+          const float2 ni = make_float2(-is.x, -is.y), nf = make_float2(-fs.x, -fs.y);
+          auto two = [&](float& a0, float& a1, float2 it, float2 ft, int l, int t) {
+            const float2 d = __fadd2_rn(__fadd2_rn(it, ni), __fadd2_rn(ft, nf));
+            const float2 y = __fmul2_rn(make_float2(a0, a1), __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), be));
+            a0 = static_cast<unsigned>(s - l) <= static_cast<unsigned>(t - l) ? y.x : 0.0f;
+            a1 = static_cast<unsigned>(s + 1 - l) <= static_cast<unsigned>(t - l) ? y.y : 0.0f;
+          };
+          two(r[4 * j], r[4 * j + 1], i0, f0, l0, t0);
+          two(r[4 * j + 2], r[4 * j + 3], i1, f1, l1, t1);
+          if constexpr (HALF) {
+            m0 = fmaxf(m0, fmaxf(fabsf(r[4 * j]), fabsf(r[4 * j + 1])));
+            m1 = fmaxf(m1, fmaxf(fabsf(r[4 * j + 2]), fabsf(r[4 * j + 3])));
+          }
+        }
+        float s0 = 1.0f, s1 = 1.0f;
+        if constexpr (HALF) {
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+          }
+          float k0, k1;
+          s0 = row_scale(m0, k0);
+          s1 = row_scale(m1, k1);
+          if (lane % 4 == 0) {
+            float* sp = reinterpret_cast<float*>(sm + L::kScaleP) + 64 * buf;
+            sp[t0] = k0;
+            sp[t1] = k1;
+          }
+        }
+        if (!wait_all(B::kPFree + buf, (n >> 1) - 1)) return false;
+        unsigned char* pb = sm + L::kP + buf * L::kPanel;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j >= 2 * (qd + 1)) continue;
+          *reinterpret_cast<uint32_t*>(pb + t0 * 128 + ((j ^ (t0 & 7)) << 4) + 2 * cc) =
+              E::narrow2(r[4 * j] * s0, r[4 * j + 1] * s0);
+          *reinterpret_cast<uint32_t*>(pb + t1 * 128 + ((j ^ (t1 & 7)) << 4) + 2 * cc) =
+              E::narrow2(r[4 * j + 2] * s1, r[4 * j + 3] * s1);
+        }
+        fence_async_smem();
+        signal(B::kPFull + buf);
+        return true;
+      };
+      bool first = true;
+      Item nx{};
+      for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+        const Item x = item_at(it);
+        const int row = x.blk * MDV + irow;
+        const bool live = irow >= 0 && row < p.dv;
+        // is there another chunk behind this item's last one?
+        int more = it + gridDim.x;
+        bool another = false;
+        for (; more < a.items; more += gridDim.x)
+          if ((nx = item_at(more)).chunks > 0) {
+            another = true;
+            break;
+          }
+        for (int c = 0; ok && c < x.chunks; ++c, ++g) {
+          if (first) {
+            if (!(ok = form_p(0))) break;
+            first = false;
+          }
+          if ((c + 1 < x.chunks || another) && !(ok = form_p(g + 1))) break;
+          if (!(ok = wait_all(B::kOFull, g))) break;
+          fence_after();
+          const int st = g % NST;
+          const float* eg = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot) + Gate::kDecay;
+          const float* sp = reinterpret_cast<const float*>(sm + L::kScaleP) + 64 * (g & 1);
+          const float ss = HALF && irow >= 0 ? reinterpret_cast<const float*>(sm + L::kScaleS)[128 * (g & 1) + irow] : 1.0f;
+          const int t = x.begin + c * C, n = x.end - t;
+          T* o = static_cast<T*>(p.o) + static_cast<size_t>(t) * p.o_stride + static_cast<size_t>(x.head) * p.dv + row;
+          const int stop = live ? n : 0;  // this lane's tokens
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float u[16], y[16];
+            tm_ld16(tw + kPtColO1 + 16 * q, u);
+            tm_ld16(tw + kPtColO2 + 16 * q, y);
+            wait_ld();
+            if (q == 3 && !HALF) {
+              fence_before();
+              signal(B::kOFree);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 d = *reinterpret_cast<const float4*>(eg + 16 * q + e);
+              if constexpr (HALF) {
+                const float4 k = *reinterpret_cast<const float4*>(sp + 16 * q + e);
+                u[e] = __fmaf_rn(d.x * ss, u[e], k.x * y[e]);
+                u[e + 1] = __fmaf_rn(d.y * ss, u[e + 1], k.y * y[e + 1]);
+                u[e + 2] = __fmaf_rn(d.z * ss, u[e + 2], k.z * y[e + 2]);
+                u[e + 3] = __fmaf_rn(d.w * ss, u[e + 3], k.w * y[e + 3]);
+              } else {
+                u[e] = __fmaf_rn(d.x, u[e], y[e]);
+                u[e + 1] = __fmaf_rn(d.y, u[e + 1], y[e + 1]);
+                u[e + 2] = __fmaf_rn(d.z, u[e + 2], y[e + 2]);
+                u[e + 3] = __fmaf_rn(d.w, u[e + 3], y[e + 3]);
+              }
+            }
+            if (n >= C) {
+              if (live) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e, o += p.o_stride) *o = E::narrow(u[e]);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e, o += p.o_stride)
+                if (16 * q + e < stop) *o = E::narrow(u[e]);
+            }
+          }
+          if constexpr (HALF) {  // the row scales are read as well
+            fence_before();
+            signal(B::kOFree);
+          }
+          signal(B::kGateFree + st);
+        }
+      }
+    }
+  } else if (warp >= 8) {
+    // ---- W(g + 1), then the state behind chunk g
+    const int half = (warp - 8) >> 2;  // which half of W's tokens and of S's columns
+    constexpr int SC = DK / 2;
+    float S[SC];
+    float wback[2] = {1.0f, 1.0f};  // fp16: what takes W's row scale out again, by chunk parity
+    int pairs = 0;
+    float worst = 0.0f;
+    // fp16: the largest of m over the two warpgroups' halves of a row, in `worst`
+    auto pair_max = [&](float m, int buf) -> bool {
+      float* mx = reinterpret_cast<float*>(sm + L::kMax) + 256 * buf;
+      if (irow >= 0) mx[128 * half + irow] = m;
+      signal(B::kPair);
+      if (!wait_all(B::kPair, pairs++)) return false;
+      worst = irow >= 0 ? fmaxf(m, mx[128 * (half ^ 1) + irow]) : 0.0f;
+      return true;
+    };
+    auto form_w = [&](int n, int count) -> bool {  // `count`: tokens left in the prompt
+      const int st = n % NST;
+      if (!wait_all(B::kFull + st, n / NST) || !wait_all(B::kGateFull + st, n / NST)) return false;
+      unsigned char* s = sm + st * L::kStage;
+      const float* w = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot) + Gate::kW + 32 * half;
+      const int left = irow >= 0 ? count - 32 * half : 0;  // of this thread's 32 tokens, the first `left` count
+      if (count < C) {
+        // the rows behind the prompt's end belong to others: zeros for the contractions
+        const int n16 = (C - count) * 8;
+        for (int i = tid - 256; i < n16 * ((DK + MDV) / 64); i += 256) {
+          const int panel = i / n16, j = i % n16;
+          *reinterpret_cast<uint4*>(s + L::kK + panel * L::kPanel + (count + j / 8) * 128 + 16 * (j % 8)) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_async_smem();
+      }
+      const int col = max(irow, 0);
+      const unsigned char* vb = s + L::kV + (col >> 6) * L::kPanel + 2 * (col & 7) + 32 * half * 128;
+      const int chunk = (col & 63) >> 3;
+      // w v of 16 tokens from j on; every load is in bounds, whatever counts
+      auto values = [&](int j, float (&x)[16]) {
+        T v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          v[i] = *reinterpret_cast<const T*>(vb + (j + i) * 128 + ((chunk ^ (i & 7)) << 4));
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(w + j + i);
+          x[i] = f.x * E::widen(v[i]);
+          x[i + 1] = f.y * E::widen(v[i + 1]);
+          x[i + 2] = f.z * E::widen(v[i + 2]);
+          x[i + 3] = f.w * E::widen(v[i + 3]);
+        }
+        if (left < 32) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = j + i < left ? x[i] : 0.0f;
+        }
+      };
+      float up = 1.0f;
+      if constexpr (HALF) {
+        float m = 0.0f;
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          float x[16];
+          values(16 * q, x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
+        }
+        if (!pair_max(m, n & 1)) return false;
+        float back;
+        up = row_scale(worst, back);
+        if (n & 1) wback[1] = back; else wback[0] = back;
+      }
+      const uint32_t at = tw + kPtColW + 64 * (n & 1) + 16 * half;
+#pragma unroll 1
+      for (int q = 0; q < 2; ++q) {
+        uint32_t hi[8], lo[8];
+        float x[16];
+        values(16 * q, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if constexpr (HALF) {
+            x[2 * j] *= up;
+            x[2 * j + 1] *= up;
+          }
+          hi[j] = E::narrow2(x[2 * j], x[2 * j + 1]);
+          const float2 h = E::widen2(hi[j]);
+          lo[j] = E::narrow2(x[2 * j] - h.x, x[2 * j + 1] - h.y);
+        }
+        tm_st8u(at + 8 * q, hi);
+        tm_st8u(at + 32 + 8 * q, lo);
+      }
+      wait_st();
+      fence_before();
+      signal(B::kWFull + (n & 1));
+      if (lane == 0) arrive(bar(B::kEmpty + st));
+      return true;
+    };
+    // the state before chunk n into tensor memory, rounded to E
+    auto put_state = [&](int n) -> bool {
+      float up = 1.0f;
+      if constexpr (HALF) {
+        float m = 0.0f, back;
+#pragma unroll
+        for (int j = 0; j < SC; ++j) m = fmaxf(m, fabsf(S[j]));
+        if (!pair_max(m, 2 + (n & 1))) return false;
+        up = row_scale(worst, back);
+        if (!wait_all(B::kO1Done, n - 1)) return false;
+        if (half == 0 && irow >= 0) reinterpret_cast<float*>(sm + L::kScaleS)[128 * (n & 1) + irow] = back;
+      } else {
+        if (!wait_all(B::kO1Done, n - 1)) return false;
+      }
+      fence_after();
+#pragma unroll
+      for (int q = 0; q < SC / 32; ++q) {
+        uint32_t r[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float u = S[32 * q + 2 * j], v = S[32 * q + 2 * j + 1];
+          r[j] = HALF ? E::narrow2(u * up, v * up) : E::narrow2(u, v);
+        }
+        tm_st16u(tw + kPtColS + half * (SC / 2) + 16 * q, r);
+      }
+      wait_st();
+      fence_before();
+      signal(B::kSFull);
+      return true;
+    };
+    bool first = true;
+    for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+      const Item x = item_at(it);
+      const int row = x.blk * MDV + irow;
+      const bool live = irow >= 0 && row < p.dv;
+      const size_t at = (static_cast<size_t>(x.tile) * p.dv + (live ? row : 0)) * DK + SC * half;
+      if (live && p.S0 != nullptr) {
+#pragma unroll
+        for (int j = 0; j < SC / 4; ++j) {
+          const float4 v = *reinterpret_cast<const float4*>(p.S0 + at + 4 * j);
+          S[4 * j] = v.x;
+          S[4 * j + 1] = v.y;
+          S[4 * j + 2] = v.z;
+          S[4 * j + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < SC; ++j) S[j] = 0.0f;
+      }
+      Item nx{};
+      bool another = false;
+      for (int more = it + gridDim.x; more < a.items; more += gridDim.x)
+        if ((nx = item_at(more)).chunks > 0) {
+          another = true;
+          break;
+        }
+      if (x.chunks > 0) {
+        if (first) ok = form_w(0, x.end - x.begin);
+        first = false;
+        if (ok && outputs) ok = put_state(g);
+      }
+      for (int c = 0; ok && c < x.chunks; ++c, ++g) {
+        if (c + 1 < x.chunks) {
+          ok = form_w(g + 1, x.end - x.begin - (c + 1) * C);
+        } else if (another) {
+          ok = form_w(g + 1, nx.end - nx.begin);
+        }
+        if (!ok || !(ok = wait_all(B::kKvFull, g))) break;
+        fence_after();
+        const int st = g % NST;
+        const float gamma = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot)[Gate::kLast];
+        const float back = (g & 1) ? wback[1] : wback[0];
+#pragma unroll
+        for (int q = 0; q < SC / 16; ++q) {
+          float r[16];
+          tm_ld16(tw + kPtColKV + SC * half + 16 * q, r);
+          wait_ld();
+          if (q == SC / 16 - 1) {
+            fence_before();
+            signal(B::kKvFree);
+            if (lane == 0) arrive(bar(B::kGateFree + st));
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            S[16 * q + e] = __fmaf_rn(S[16 * q + e], gamma, HALF ? r[e] * back : r[e]);
+        }
+        if (outputs && c + 1 < x.chunks) ok = put_state(g + 1);
+      }
+      if (ok && live) {
+#pragma unroll
+        for (int j = 0; j < SC / 4; ++j)
+          *reinterpret_cast<float4*>(p.S1 + at + 4 * j) = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+      }
+    }
+  }
+
+  __syncwarp();
+  if (!ok) *failed = 1;
+  __syncthreads();
+  if (tid == 0 && *failed) atomicAdd(&packed_timeouts, 1u);
+  fence_after();
+  // After a timeout a contraction may still write the columns freed here:
+  // the launch's outputs are undefined then, and the count tells.
+  if (warp == 3) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512u) : "memory");
+}
+
+}  // namespace qs

@@ -11,8 +11,6 @@
 
 namespace qs {
 
-inline size_t dtype_bytes(int dtype) { return dtype == QS_F32 ? 4 : 2; }
-
 // The element types as tags: `bits` is what memory holds, widen/narrow are
 // exact / rounded to nearest even.
 struct F32 {

@@ -34,6 +34,7 @@ EXPORTS = ("qstate_query_sizes", "qstate_init", "qstate_decode_step", "qstate_re
            "qstate_state_sq_norms", "qstate_fp32_sq_norms",
            "qstate_cache_write", "qstate_cache_read", "qstate_cache_step",
            "qstate_prefill_packed_workspace", "qstate_prefill_packed",
+           "qstate_prefill_packed_timeouts",
            "qstate_selfcheck", "qstate_status_string", "qstate_version")
 
 
@@ -94,6 +95,7 @@ def lib() -> ctypes.CDLL:
         L.qstate_cache_step.argtypes = [C, B] + [P] * 10
         L.qstate_prefill_packed_workspace.argtypes = [C, B, ctypes.c_int, sz]
         L.qstate_prefill_packed.argtypes = [C, B, ctypes.c_int] + [P] * 10 + [ctypes.c_size_t, P]
+        L.qstate_prefill_packed_timeouts.argtypes = [P]
         for f in (L.qstate_query_sizes, L.qstate_init, L.qstate_decode_step, L.qstate_readout,
                   L.qstate_selfcheck, L.qstate_fp32_decode_step, L.qstate_state_sq_norms,
                   L.qstate_fp32_sq_norms, L.qstate_lrb_query_sizes, L.qstate_lrb_decode_step,
@@ -102,7 +104,8 @@ def lib() -> ctypes.CDLL:
                   L.qstate_pipeline_create, L.qstate_pipeline_step, L.qstate_pipeline_wait_stream,
                   L.qstate_pipeline_join, L.qstate_pipeline_sync, L.qstate_pipeline_destroy,
                   L.qstate_decode_step_host_static, L.qstate_cache_write, L.qstate_cache_read,
-                  L.qstate_cache_step, L.qstate_prefill_packed_workspace, L.qstate_prefill_packed):
+                  L.qstate_cache_step, L.qstate_prefill_packed_workspace, L.qstate_prefill_packed,
+                  L.qstate_prefill_packed_timeouts):
             f.restype = ctypes.c_int
         L.qstate_status_string.argtypes = [ctypes.c_int]
         L.qstate_status_string.restype = ctypes.c_char_p
@@ -576,6 +579,13 @@ class PackedPrefill(_OnDevice):
                       v.data_ptr(), alpha.data_ptr(), beta.data_ptr(), _ptr(o), self.workspace.data_ptr(),
                       self.workspace.numel()), stream)
         return o, S
+
+
+def prefill_packed_timeouts() -> int:
+    """CTAs of PackedPrefill.run whose bounded wait gave up since the library was loaded (0 in order)."""
+    n = ctypes.c_uint(0)
+    _check(lib().qstate_prefill_packed_timeouts(ctypes.byref(n)), "qstate_prefill_packed_timeouts")
+    return n.value
 
 
 def packed_workspace(cfg: Config, tokens: int, heads: int, qk_heads: int, sequences: int) -> int:

@@ -123,6 +123,10 @@ def test_packed_limits():
     assert _packed(sequences=(1 << 31) - 1) == Q.QS_ERR_UNSUPPORTED
 
 
+def test_timeout_count_needs_a_place():
+    assert Q.lib().qstate_prefill_packed_timeouts(None) == Q.QS_ERR_INVALID_ARG
+
+
 def test_workspace_grows_with_the_batch():
     sizes = [Q.packed_workspace(_cfg(), t, 4, 2, n) for t, n in ((0, 0), (1, 1), (64, 1), (1000, 1), (1000, 4),
                                                                 (30000, 4), (30000, 64))]

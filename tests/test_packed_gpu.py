@@ -23,6 +23,13 @@ HALF = {F32: 0.0, F16: 2.0 ** -11, BF16: 2.0 ** -8}
 STATE = 2.0 ** -14
 
 
+@pytest.fixture(autouse=True)
+def _no_wait_gave_up():
+    yield
+    from ssm_decode_step_b200 import qstate as Q
+    assert Q.prefill_packed_timeouts() == 0
+
+
 def _cfg(dk, dv):
     from ssm_decode_step_b200 import Config
     return Config(0, dk, dv, 8, 32, 0)
