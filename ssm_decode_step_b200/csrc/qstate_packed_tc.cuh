@@ -44,6 +44,7 @@
 
 #include <cuda.h>
 
+#include "qstate_cache.cuh"
 #include "qstate_packed.cuh"
 #include "qstate_prefill_tc.cuh"
 
@@ -55,10 +56,29 @@ constexpr int kPtChunk = 64;
 constexpr uint32_t kPtColScore = 0, kPtColO1 = 64, kPtColO2 = 128, kPtColKV = 192, kPtColS = 320, kPtColW = 384;
 constexpr float kPtReset = 0x1p-120f;
 
+// Few prompts and heads leave most SMs without an item.  Then a prompt longer
+// than `seg` tokens is cut into segments of that length, and three launches
+// share the work: the states that the segments would leave from a zero state
+// (all but a prompt's last one), a pass that joins them in order into the
+// state before each segment, and the prefill of every segment from there.
+// Unit u of the work is segment u - (starts[i] / seg + i) of the last prompt
+// i with starts[i] / seg + i <= u, which leaves room for every prompt's
+// segments without a table; units behind them are empty.  A segment that
+// has a successor is `seg` tokens long, so its first token / seg numbers
+// the stored states without gaps or clashes.
 struct PackedTcParams {
   PackedParams p;
-  int items;  // prompts * heads * row blocks
+  int items;      // units * heads * row blocks
+  int sequences;
+  int seg;        // tokens of a segment, a multiple of the chunk; 0: prompts are not cut
+  bool local;     // the first of the three launches
+  float* states;  // [tokens / seg + 1][heads][Dv][Dk]
+  float* decays;  // [tokens / seg + 1][heads]: the segment's whole decay
 };
+
+__device__ __forceinline__ int prompt_segments(int begin, int end, int seg) {
+  return end > begin ? (end - begin + seg - 1) / seg : 1;
+}
 
 // Shared memory of a CTA (byte offsets from a 1024-byte boundary).
 template <int DK, int MDV>
@@ -71,8 +91,8 @@ struct PtLayout {
   static constexpr int kGateSlot = 6 * 256 + 128;
   static constexpr int kScaleS = kGate + kStages * kGateSlot;  // fp16: 2 x 128 row scales of S
   static constexpr int kScaleP = kScaleS + 1024;               // fp16: 2 x 64 row scales of P
-  static constexpr int kMax = kScaleP + 512;                   // fp16: 4 x 2 x 128 row maxima
-  static constexpr int kBars = kMax + 4096;
+  static constexpr int kMax = kScaleP + 512;                   // fp16: 6 x 2 x 128 row maxima, 4 of W and 2 of S
+  static constexpr int kBars = kMax + 6144;
   static constexpr int kBytes = kBars + 320 + 1024;
 };
 
@@ -114,12 +134,12 @@ __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lbo) {
 }
 
 // One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t p;
   asm volatile(
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(p));
-  return p != 0;
+  return p;
 }
 
 // One look at the phase of the given parity.
@@ -145,18 +165,27 @@ static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity
   return false;
 }
 
-__device__ __forceinline__ void mma16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+// The issuing instructions are predicated rather than branched around, which
+// keeps the warp together and their operands uniform.
+__device__ __forceinline__ void mma16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t mbar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(mbar),
+      "r"(lead)
       : "memory");
 }
 
@@ -198,9 +227,29 @@ __device__ __forceinline__ void tm_st16u(uint32_t addr, const uint32_t (&r)[16])
       : "memory");
 }
 
-__device__ __forceinline__ void tm_st8u(uint32_t addr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+// 16 lanes x 16 columns from all 32 threads: registers 2j and 2j + 1 are
+// column 4j + T%4 of rows T/4 and T/4 + 8.
+__device__ __forceinline__ void tm_st_16x16(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// Four 8 x 8 matrices of 16-bit elements, transposed: thread T holds elements
+// 2 (T%4) and the next of memory rows, at column T/4.
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stsm4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void tma_store3(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+               "r"(y), "r"(z), "r"(src)
                : "memory");
 }
 
@@ -228,7 +277,8 @@ static __device__ unsigned int packed_timeouts = 0;
 template <class E, int DK, int MDV>
 __global__ void __launch_bounds__(kPtThreads, 1)
     packed_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                     const __grid_constant__ CUtensorMap mv, const PackedTcParams a) {
+                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+                     const PackedTcParams a) {
   using namespace pt;
   using L = PtLayout<DK, MDV>;
   constexpr int NST = L::kStages;
@@ -256,7 +306,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) {
       bar_init(bar(B::kFull + s), 1);
-      bar_init(bar(B::kEmpty + s), 1 + 8);                   // the contractions; W's warps
+      bar_init(bar(B::kEmpty + s), outputs ? 4 + 8 : 1 + 8);  // the outputs' warps, or the contractions; W's warps
       bar_init(bar(B::kGateFull + s), 1);
       bar_init(bar(B::kGateFree + s), outputs ? 4 + 8 : 8);  // its readers
     }
@@ -308,19 +358,65 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   };
 
   struct Item {
-    int tile, head, blk, begin, end, chunks;
+    int head, blk, begin, end, chunks;
+    const float* from;  // the head's state before the item (null: zeros)
+    float* to;          // and where it goes after it (null: nowhere)
+    float* decay;       // where the item's whole decay goes (null: nowhere)
   };
   auto item_at = [&](int it) {
     Item x;
     x.blk = it % p.blocks;
-    x.tile = it / p.blocks;
-    const int seq = x.tile / p.heads;
-    x.head = x.tile - seq * p.heads;
+    const int r = it / p.blocks;
+    int seq = r / p.heads, seg = 0;
+    x.head = r - seq * p.heads;
+    const size_t tile = static_cast<size_t>(p.dv) * DK;
+    if (a.seg > 0) {
+      const int unit = seq;
+      auto first = [&](int i) { return min(max(__ldg(p.starts + i), 0), p.tokens) / a.seg + i; };
+      int lo = 0, hi = a.sequences - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first(mid) <= unit) lo = mid; else hi = mid - 1;
+      }
+      seq = lo;
+      seg = unit - first(lo);
+    }
     prompt_bounds(p.starts, seq, p.tokens, x.begin, x.end);
+    const size_t at = (static_cast<size_t>(seq) * p.heads + x.head) * tile;
+    x.from = p.S0 == nullptr ? nullptr : p.S0 + at;
+    x.to = p.S1 + at;
+    x.decay = nullptr;
+    if (a.seg > 0) {
+      const int segs = prompt_segments(x.begin, x.end, a.seg);
+      auto stored = [&](int k) { return static_cast<size_t>((x.begin + k * a.seg) / a.seg) * p.heads + x.head; };
+      const bool last = seg >= segs - 1;
+      if (seg < 0 || seg >= segs || (a.local && last)) {
+        x.end = x.begin;
+        x.to = nullptr;
+      } else if (a.local) {
+        x.from = nullptr;
+        x.to = a.states + stored(seg) * tile;
+        x.decay = a.decays + stored(seg);
+      } else {
+        if (seg > 0) x.from = a.states + stored(seg - 1) * tile;
+        if (!last) x.to = nullptr;
+      }
+      if (seg > 0) x.begin += seg * a.seg;
+      if (!last) x.end = min(x.end, x.begin + a.seg);
+      x.end = max(x.end, x.begin);
+    }
     x.chunks = (x.end - x.begin + C - 1) / C;
     return x;
   };
-  const int irow = tc_row<MDV>(qd, lane);  // row of W, S and the outputs of this lane
+  // Tokens of the CTA's next item behind `it` that has any; 0: none has.
+  auto count_behind = [&](int it) {
+    for (it += gridDim.x; it < a.items; it += gridDim.x) {
+      const Item x = item_at(it);
+      if (x.chunks > 0) return x.end - x.begin;
+    }
+    return 0;
+  };
+  const int irow = tc_row<MDV>(qd, lane);  // row of S of this lane
 
   bool ok = true;
   int g = 0;  // chunks so far, over all items of this CTA
@@ -356,19 +452,17 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const uint64_t dq = desc128(base + L::kQ, 16), dk = desc128(base + L::kK, 16),
                    dkt = desc128(base + L::kK, L::kPanel), dv = desc128(base + L::kV, L::kPanel),
                    dp = desc128(base + L::kP, 16);
-    const bool lead = elect_one();
+    const uint32_t lead = elect_one();
     auto scores = [&](int n) -> bool {
       const uint32_t s = (n % NST) * (L::kStage / 16);
       if (!wait_all(B::kFull + n % NST, n / NST) || !wait_all(B::kScFree, n - 1)) return false;
       fence_after();
-      if (lead) {
 #pragma unroll
-        for (int k = 0; k < DK / 16; ++k) {
-          const uint32_t off = s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16;
-          mma16_ss(tm + kPtColScore, dq + off, dk + off, id_sc, k > 0);
-        }
-        mma_commit(bar(B::kScFull));
+      for (int k = 0; k < DK / 16; ++k) {
+        const uint32_t off = s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16;
+        mma16_ss(tm + kPtColScore, dq + off, dk + off, id_sc, k > 0, lead);
       }
+      commit_if(bar(B::kScFull), lead);
       return true;
     };
     int total = 0;
@@ -378,40 +472,35 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     for (; ok && g < total; ++g) {
       const int st = g % NST;
       const uint32_t s = st * (L::kStage / 16);
-      if (!(ok = wait_all(B::kFull + st, g / NST) && wait_all(B::kWFull + (g & 1), g >> 1) && wait_all(B::kKvFree, g - 1)))
-        break;
+      // W's warps have waited for this stage's loads; so have the scores
+      if (!(ok = wait_all(B::kWFull + (g & 1), g >> 1) && wait_all(B::kKvFree, g - 1))) break;
+      if (!outputs && !(ok = wait_all(B::kFull + st, g / NST))) break;
       fence_after();
-      if (lead) {
-        const uint32_t w = tm + kPtColW + 64 * (g & 1);
+      const uint32_t w = tm + kPtColW + 64 * (g & 1);
 #pragma unroll
-        for (int k = 0; k < C / 8; ++k)  // 4 steps of W's value, 4 of its rounding error
-          mma16_ts(tm + kPtColKV, w + 8 * k, dkt + (s + (k % 4) * (2048 / 16)), id_kv, k > 0);
-        mma_commit(bar(B::kKvFull));
-      }
+      for (int k = 0; k < C / 8; ++k)  // 4 steps of W's value, 4 of its rounding error
+        mma16_ts(tm + kPtColKV, w + 8 * k, dkt + (s + (k % 4) * (2048 / 16)), id_kv, k > 0, lead);
+      commit_if(bar(B::kKvFull), lead);
       if (outputs) {
         if (!(ok = wait_all(B::kSFull, g) && wait_all(B::kOFree, g - 1))) break;
         fence_after();
-        if (lead) {
 #pragma unroll
-          for (int k = 0; k < DK / 16; ++k)
-            mma16_ts(tm + kPtColO1, tm + kPtColS + 8 * k, dq + (s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16), id_o1,
-                     k > 0);
-          mma_commit(bar(B::kO1Done));
-        }
+        for (int k = 0; k < DK / 16; ++k)
+          mma16_ts(tm + kPtColO1, tm + kPtColS + 8 * k, dq + (s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16), id_o1, k > 0,
+                   lead);
+        commit_if(bar(B::kO1Done), lead);
         if (g + 1 < total && !(ok = scores(g + 1))) break;
         if (!(ok = wait_all(B::kPFull + (g & 1), g >> 1))) break;
         fence_after();
-        if (lead) {
-          const uint32_t pb = (g & 1) * (L::kPanel / 16);
+        const uint32_t pb = (g & 1) * (L::kPanel / 16);
 #pragma unroll
-          for (int k = 0; k < C / 16; ++k)
-            mma16_ss(tm + kPtColO2, dv + (s + k * (2048 / 16)), dp + (pb + 2 * k), id_o2, k > 0);
-          mma_commit(bar(B::kOFull));
-          mma_commit(bar(B::kPFree + (g & 1)));
-        }
+        for (int k = 0; k < C / 16; ++k)
+          mma16_ss(tm + kPtColO2, dv + (s + k * (2048 / 16)), dp + (pb + 2 * k), id_o2, k > 0, lead);
+        commit_if(bar(B::kOFull), lead);
+        commit_if(bar(B::kPFree + (g & 1)), lead);
+      } else {
+        commit_if(bar(B::kEmpty + st), lead);
       }
-      if (lead) mma_commit(bar(B::kEmpty + st));
-      __syncwarp();
     }
   } else if (warp == 2) {
     // ---- the chunk's factors from alpha and beta, one chunk's loads ahead
@@ -550,72 +639,85 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         signal(B::kPFull + buf);
         return true;
       };
-      bool first = true;
-      Item nx{};
+      constexpr int WR = MDV / 4;  // rows of a warp
       for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
         const Item x = item_at(it);
-        const int row = x.blk * MDV + irow;
-        const bool live = irow >= 0 && row < p.dv;
-        // is there another chunk behind this item's last one?
-        int more = it + gridDim.x;
-        bool another = false;
-        for (; more < a.items; more += gridDim.x)
-          if ((nx = item_at(more)).chunks > 0) {
-            another = true;
-            break;
-          }
         for (int c = 0; ok && c < x.chunks; ++c, ++g) {
-          if (first) {
-            if (!(ok = form_p(0))) break;
-            first = false;
-          }
-          if ((c + 1 < x.chunks || another) && !(ok = form_p(g + 1))) break;
+          if (g == 0 && !(ok = form_p(0))) break;
+          if ((c + 1 < x.chunks || count_behind(it) > 0) && !(ok = form_p(g + 1))) break;
           if (!(ok = wait_all(B::kOFull, g))) break;
           fence_after();
           const int st = g % NST;
           const float* eg = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot) + Gate::kDecay;
           const float* sp = reinterpret_cast<const float*>(sm + L::kScaleP) + 64 * (g & 1);
-          const float ss = HALF && irow >= 0 ? reinterpret_cast<const float*>(sm + L::kScaleS)[128 * (g & 1) + irow] : 1.0f;
+          const float* ss = reinterpret_cast<const float*>(sm + L::kScaleS) + 128 * (g & 1) + WR * qd;
           const int t = x.begin + c * C, n = x.end - t;
-          T* o = static_cast<T*>(p.o) + static_cast<size_t>(t) * p.o_stride + static_cast<size_t>(x.head) * p.dv + row;
-          const int stop = live ? n : 0;  // this lane's tokens
+          // the contractions are done with q and k: their place holds this
+          // warp's outputs [64 tokens][WR rows], swizzled as the store wants
+          const uint32_t out = base + st * L::kStage + qd * (C * WR * 2);
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            float u[16], y[16];
-            tm_ld16(tw + kPtColO1 + 16 * q, u);
-            tm_ld16(tw + kPtColO2 + 16 * q, y);
+          for (int h = 0; h < WR / 16; ++h) {
+            float u[32], y[32];
+            tm_ld_16x64(tw + (static_cast<uint32_t>(16 * h) << 16) + kPtColO1, u);
+            tm_ld_16x64(tw + (static_cast<uint32_t>(16 * h) << 16) + kPtColO2, y);
             wait_ld();
-            if (q == 3 && !HALF) {
+            if (h == WR / 16 - 1 && !HALF) {
               fence_before();
               signal(B::kOFree);
             }
+            const float sa = HALF ? ss[16 * h + lane / 4] : 1.0f, sb = HALF ? ss[16 * h + 8 + lane / 4] : 1.0f;
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 d = *reinterpret_cast<const float4*>(eg + 16 * q + e);
+            for (int j = 0; j < 8; ++j) {
+              const float2 d = *reinterpret_cast<const float2*>(eg + 8 * j + 2 * (lane % 4));
+              float2 ya = make_float2(y[4 * j], y[4 * j + 1]), yb = make_float2(y[4 * j + 2], y[4 * j + 3]);
+              float2 da = d, db = d;
               if constexpr (HALF) {
-                const float4 k = *reinterpret_cast<const float4*>(sp + 16 * q + e);
-                u[e] = __fmaf_rn(d.x * ss, u[e], k.x * y[e]);
-                u[e + 1] = __fmaf_rn(d.y * ss, u[e + 1], k.y * y[e + 1]);
-                u[e + 2] = __fmaf_rn(d.z * ss, u[e + 2], k.z * y[e + 2]);
-                u[e + 3] = __fmaf_rn(d.w * ss, u[e + 3], k.w * y[e + 3]);
-              } else {
-                u[e] = __fmaf_rn(d.x, u[e], y[e]);
-                u[e + 1] = __fmaf_rn(d.y, u[e + 1], y[e + 1]);
-                u[e + 2] = __fmaf_rn(d.z, u[e + 2], y[e + 2]);
-                u[e + 3] = __fmaf_rn(d.w, u[e + 3], y[e + 3]);
+                const float2 k = *reinterpret_cast<const float2*>(sp + 8 * j + 2 * (lane % 4));
+                ya = __fmul2_rn(k, ya);
+                yb = __fmul2_rn(k, yb);
+                da = __fmul2_rn(d, f2(sa));
+                db = __fmul2_rn(d, f2(sb));
               }
+              const float2 oa = __ffma2_rn(da, make_float2(u[4 * j], u[4 * j + 1]), ya);
+              const float2 ob = __ffma2_rn(db, make_float2(u[4 * j + 2], u[4 * j + 3]), yb);
+              w[2 * j] = E::narrow2(oa.x, oa.y);
+              w[2 * j + 1] = E::narrow2(ob.x, ob.y);
             }
-            if (n >= C) {
-              if (live) {
+            // matrices: rows 16h.. and 16h + 8.. of two blocks of 8 tokens
+            const int m = lane >> 3, chunk = 2 * h + (m & 1);
 #pragma unroll
-                for (int e = 0; e < 16; ++e, o += p.o_stride) *o = E::narrow(u[e]);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e, o += p.o_stride)
-                if (16 * q + e < stop) *o = E::narrow(u[e]);
+            for (int j = 0; j < 8; j += 2) {
+              const int tt = 8 * (j + (m >> 1)) + (lane & 7);
+              const int sw = WR == 32 ? (tt >> 1) & 3 : (tt >> 2) & 1;
+              stsm4_t(out + tt * (2 * WR) + ((chunk ^ sw) << 4), w[2 * j], w[2 * j + 1], w[2 * j + 2], w[2 * j + 3]);
             }
           }
+          fence_async_smem();
+          __syncwarp();
+          const int row = x.blk * MDV + WR * qd;  // the warp's first row
+          if (n >= C) {
+            if (lane == 0 && row < p.dv) tma_store3(&mo, out, row, x.head, t);
+          } else {
+            // a prompt's end: only its own rows
+            constexpr int PER = WR / 8;  // 16-byte pieces of a token
+            const int piece = lane % PER;
+            if (row + 8 * piece < p.dv) {
+              T* o = static_cast<T*>(p.o) + static_cast<size_t>(t) * p.o_stride + static_cast<size_t>(x.head) * p.dv + row +
+                     8 * piece;
+              for (int tt = lane / PER; tt < n; tt += 32 / PER) {
+                const int sw = WR == 32 ? (tt >> 1) & 3 : (tt >> 2) & 1;
+                *reinterpret_cast<uint4*>(o + tt * p.o_stride) = *reinterpret_cast<const uint4*>(
+                    sm + (out - base) + tt * (2 * WR) + ((piece ^ sw) << 4));
+              }
+            }
+          }
+          // the stage before this one is free once its store has read it
+          if (lane == 0) {
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          }
+          if (g > 0) signal(B::kEmpty + (g - 1) % NST);
           if constexpr (HALF) {  // the row scales are read as well
             fence_before();
             signal(B::kOFree);
@@ -628,90 +730,112 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     // ---- W(g + 1), then the state behind chunk g
     const int half = (warp - 8) >> 2;  // which half of W's tokens and of S's columns
     constexpr int SC = DK / 2;
-    float S[SC];
-    float wback[2] = {1.0f, 1.0f};  // fp16: what takes W's row scale out again, by chunk parity
+    float2 S[SC / 2];
     int pairs = 0;
-    float worst = 0.0f;
-    // fp16: the largest of m over the two warpgroups' halves of a row, in `worst`
-    auto pair_max = [&](float m, int buf) -> bool {
-      float* mx = reinterpret_cast<float*>(sm + L::kMax) + 256 * buf;
-      if (irow >= 0) mx[128 * half + irow] = m;
+    float* const maxima = reinterpret_cast<float*>(sm + L::kMax);
+    // fp16: both warpgroups have put down their halves' row maxima
+    auto pair = [&]() -> bool {
       signal(B::kPair);
-      if (!wait_all(B::kPair, pairs++)) return false;
-      worst = irow >= 0 ? fmaxf(m, mx[128 * (half ^ 1) + irow]) : 0.0f;
-      return true;
+      return wait_all(B::kPair, pairs++);
     };
+    auto worst = [&](int buf, int row) { return fmaxf(maxima[256 * buf + row], maxima[256 * buf + 128 + row]); };
+    // A thread holds rows T/4 and T/4 + 8 of each 16, tokens 8j + 2 (T%4)
+    // and the next of the warpgroup's 32.
     auto form_w = [&](int n, int count) -> bool {  // `count`: tokens left in the prompt
       const int st = n % NST;
       if (!wait_all(B::kFull + st, n / NST) || !wait_all(B::kGateFull + st, n / NST)) return false;
-      unsigned char* s = sm + st * L::kStage;
-      const float* w = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot) + Gate::kW + 32 * half;
-      const int left = irow >= 0 ? count - 32 * half : 0;  // of this thread's 32 tokens, the first `left` count
+      const uint32_t s = base + st * L::kStage;
       if (count < C) {
         // the rows behind the prompt's end belong to others: zeros for the contractions
         const int n16 = (C - count) * 8;
         for (int i = tid - 256; i < n16 * ((DK + MDV) / 64); i += 256) {
           const int panel = i / n16, j = i % n16;
-          *reinterpret_cast<uint4*>(s + L::kK + panel * L::kPanel + (count + j / 8) * 128 + 16 * (j % 8)) =
-              make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(sm + st * L::kStage + L::kK + panel * L::kPanel + (count + j / 8) * 128 +
+                                    16 * (j % 8)) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_async_smem();
       }
-      const int col = max(irow, 0);
-      const unsigned char* vb = s + L::kV + (col >> 6) * L::kPanel + 2 * (col & 7) + 32 * half * 128;
-      const int chunk = (col & 63) >> 3;
-      // w v of 16 tokens from j on; every load is in bounds, whatever counts
-      auto values = [&](int j, float (&x)[16]) {
-        T v[16];
+      float2 w[4];
+      {
+        const float* f = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot) + Gate::kW + 32 * half;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          v[i] = *reinterpret_cast<const T*>(vb + (j + i) * 128 + ((chunk ^ (i & 7)) << 4));
+        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const float2*>(f + 8 * j + 2 * (lane % 4));
+      }
+      // w v of row half h (16 rows): pairs of tokens, [j][0] row T/4, [j][1] row T/4 + 8
+      auto values = [&](int h, float2 (&x)[4][2]) {
+        const int col = (MDV / 4) * qd + 16 * h;  // first row of S, a column of v
+        const uint32_t panel = s + L::kV + (col >> 6) * L::kPanel + 32 * half * 128;
+        const int m = lane >> 3, chunk = ((col & 63) >> 3) + (m & 1);
+        uint32_t r[4][2];
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(w + j + i);
-          x[i] = f.x * E::widen(v[i]);
-          x[i + 1] = f.y * E::widen(v[i + 1]);
-          x[i + 2] = f.z * E::widen(v[i + 2]);
-          x[i + 3] = f.w * E::widen(v[i + 3]);
+        for (int j = 0; j < 4; j += 2) {
+          const int t = 8 * (j + (m >> 1)) + (lane & 7);
+          ldsm4_t(panel + t * 128 + ((chunk ^ (t & 7)) << 4), r[j][0], r[j][1], r[j + 1][0], r[j + 1][1]);
         }
-        if (left < 32) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = j + i < left ? x[i] : 0.0f;
+        for (int j = 0; j < 4; ++j) {
+          x[j][0] = __fmul2_rn(w[j], E::widen2(r[j][0]));
+          x[j][1] = __fmul2_rn(w[j], E::widen2(r[j][1]));
+        }
+        if (count < C) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int t = 32 * half + 8 * j + 2 * (lane % 4);
+            if (t >= count) x[j][0].x = x[j][1].x = 0.0f;
+            if (t + 1 >= count) x[j][0].y = x[j][1].y = 0.0f;
+          }
         }
       };
-      float up = 1.0f;
       if constexpr (HALF) {
-        float m = 0.0f;
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          float x[16];
-          values(16 * q, x);
+        for (int h = 0; h < MDV / 64; ++h) {
+          float2 x[4][2];
+          values(h, x);
+          float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
+          for (int j = 0; j < 4; ++j) {
+            m0 = fmaxf(m0, fmaxf(fabsf(x[j][0].x), fabsf(x[j][0].y)));
+            m1 = fmaxf(m1, fmaxf(fabsf(x[j][1].x), fabsf(x[j][1].y)));
+          }
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+          }
+          if (lane % 4 == 0) {
+            float* mx = maxima + 256 * (n & 3) + 128 * half + (MDV / 4) * qd + 16 * h + lane / 4;
+            mx[0] = m0;
+            mx[8] = m1;
+          }
         }
-        if (!pair_max(m, n & 1)) return false;
-        float back;
-        up = row_scale(worst, back);
-        if (n & 1) wback[1] = back; else wback[0] = back;
+        if (!pair()) return false;
       }
       const uint32_t at = tw + kPtColW + 64 * (n & 1) + 16 * half;
 #pragma unroll 1
-      for (int q = 0; q < 2; ++q) {
+      for (int h = 0; h < MDV / 64; ++h) {
+        float2 x[4][2];
+        values(h, x);
+        if constexpr (HALF) {
+          const int row = (MDV / 4) * qd + 16 * h + lane / 4;
+          float back;
+          const float u0 = row_scale(worst(n & 3, row), back), u1 = row_scale(worst(n & 3, row + 8), back);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[j][0] = __fmul2_rn(x[j][0], f2(u0));
+            x[j][1] = __fmul2_rn(x[j][1], f2(u1));
+          }
+        }
         uint32_t hi[8], lo[8];
-        float x[16];
-        values(16 * q, x);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if constexpr (HALF) {
-            x[2 * j] *= up;
-            x[2 * j + 1] *= up;
-          }
-          hi[j] = E::narrow2(x[2 * j], x[2 * j + 1]);
-          const float2 h = E::widen2(hi[j]);
-          lo[j] = E::narrow2(x[2 * j] - h.x, x[2 * j + 1] - h.y);
+          const float2 v = x[j / 2][j % 2];
+          hi[j] = E::narrow2(v.x, v.y);
+          const float2 k = E::widen2(hi[j]);
+          lo[j] = E::narrow2(v.x - k.x, v.y - k.y);
         }
-        tm_st8u(at + 8 * q, hi);
-        tm_st8u(at + 32 + 8 * q, lo);
+        const uint32_t to = at + (static_cast<uint32_t>(16 * h) << 16);
+        tm_st_16x16(to, hi);
+        tm_st_16x16(to + 32, lo);
       }
       wait_st();
       fence_before();
@@ -725,9 +849,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       if constexpr (HALF) {
         float m = 0.0f, back;
 #pragma unroll
-        for (int j = 0; j < SC; ++j) m = fmaxf(m, fabsf(S[j]));
-        if (!pair_max(m, 2 + (n & 1))) return false;
-        up = row_scale(worst, back);
+        for (int j = 0; j < SC / 2; ++j) m = fmaxf(m, fmaxf(fabsf(S[j].x), fabsf(S[j].y)));
+        const int buf = 4 + (n & 1);
+        if (irow >= 0) maxima[256 * buf + 128 * half + irow] = m;
+        if (!pair()) return false;
+        up = row_scale(worst(buf, max(irow, 0)), back);
         if (!wait_all(B::kO1Done, n - 1)) return false;
         if (half == 0 && irow >= 0) reinterpret_cast<float*>(sm + L::kScaleS)[128 * (n & 1) + irow] = back;
       } else {
@@ -739,8 +865,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         uint32_t r[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float u = S[32 * q + 2 * j], v = S[32 * q + 2 * j + 1];
-          r[j] = HALF ? E::narrow2(u * up, v * up) : E::narrow2(u, v);
+          const float2 u = S[16 * q + j];
+          r[j] = HALF ? E::narrow2(u.x * up, u.y * up) : E::narrow2(u.x, u.y);
         }
         tm_st16u(tw + kPtColS + half * (SC / 2) + 16 * q, r);
       }
@@ -749,48 +875,40 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       signal(B::kSFull);
       return true;
     };
-    bool first = true;
     for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
       const Item x = item_at(it);
       const int row = x.blk * MDV + irow;
       const bool live = irow >= 0 && row < p.dv;
-      const size_t at = (static_cast<size_t>(x.tile) * p.dv + (live ? row : 0)) * DK + SC * half;
-      if (live && p.S0 != nullptr) {
+      const size_t at = static_cast<size_t>(live ? row : 0) * DK + SC * half;
+      float decay = 1.0f;  // of the item so far
+      if (x.to != nullptr || x.chunks > 0) {
+        if (live && x.from != nullptr) {
 #pragma unroll
-        for (int j = 0; j < SC / 4; ++j) {
-          const float4 v = *reinterpret_cast<const float4*>(p.S0 + at + 4 * j);
-          S[4 * j] = v.x;
-          S[4 * j + 1] = v.y;
-          S[4 * j + 2] = v.z;
-          S[4 * j + 3] = v.w;
+          for (int j = 0; j < SC; j += 8) {
+            float v[8];
+            load8<F32>(v, x.from + at + j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[j / 2 + i] = make_float2(v[2 * i], v[2 * i + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < SC / 2; ++j) S[j] = f2(0.0f);
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < SC; ++j) S[j] = 0.0f;
       }
-      Item nx{};
-      bool another = false;
-      for (int more = it + gridDim.x; more < a.items; more += gridDim.x)
-        if ((nx = item_at(more)).chunks > 0) {
-          another = true;
-          break;
-        }
       if (x.chunks > 0) {
-        if (first) ok = form_w(0, x.end - x.begin);
-        first = false;
+        if (g == 0) ok = form_w(0, x.end - x.begin);
         if (ok && outputs) ok = put_state(g);
       }
       for (int c = 0; ok && c < x.chunks; ++c, ++g) {
-        if (c + 1 < x.chunks) {
-          ok = form_w(g + 1, x.end - x.begin - (c + 1) * C);
-        } else if (another) {
-          ok = form_w(g + 1, nx.end - nx.begin);
-        }
+        const int count = c + 1 < x.chunks ? x.end - x.begin - (c + 1) * C : count_behind(it);
+        if (count > 0) ok = form_w(g + 1, count);
         if (!ok || !(ok = wait_all(B::kKvFull, g))) break;
         fence_after();
         const int st = g % NST;
         const float gamma = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot)[Gate::kLast];
-        const float back = (g & 1) ? wback[1] : wback[0];
+        float back = 1.0f;
+        if constexpr (HALF) row_scale(worst(g & 3, max(irow, 0)), back);
+        decay *= gamma;
 #pragma unroll
         for (int q = 0; q < SC / 16; ++q) {
           float r[16];
@@ -802,19 +920,32 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (lane == 0) arrive(bar(B::kGateFree + st));
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            S[16 * q + e] = __fmaf_rn(S[16 * q + e], gamma, HALF ? r[e] * back : r[e]);
+          for (int e = 0; e < 8; ++e) {
+            float2 v = make_float2(r[2 * e], r[2 * e + 1]);
+            if constexpr (HALF) v = __fmul2_rn(v, f2(back));
+            S[8 * q + e] = __ffma2_rn(S[8 * q + e], f2(gamma), v);
+          }
         }
         if (outputs && c + 1 < x.chunks) ok = put_state(g + 1);
       }
-      if (ok && live) {
+      if (ok && live && x.to != nullptr) {
 #pragma unroll
-        for (int j = 0; j < SC / 4; ++j)
-          *reinterpret_cast<float4*>(p.S1 + at + 4 * j) = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+        for (int j = 0; j < SC; j += 8) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[2 * i] = S[j / 2 + i].x;
+            v[2 * i + 1] = S[j / 2 + i].y;
+          }
+          store8<F32>(x.to + at + j, v);
+        }
       }
+      if (ok && x.decay != nullptr && tid == 256 && x.blk == 0) *x.decay = decay;
     }
   }
 
+  // the outputs' stores have read shared memory before it goes
+  if (warp >= 4 && warp < 8 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncwarp();
   if (!ok) *failed = 1;
   __syncthreads();
@@ -823,6 +954,47 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   // After a timeout a contraction may still write the columns freed here:
   // the launch's outputs are undefined then, and the count tells.
   if (warp == 3) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512u) : "memory");
+}
+
+// The states that segments left from zero, joined in order: stored state k of
+// a prompt becomes the state after its segment k.  A thread owns four
+// elements of a head's state (`quads` CTAs a state); the segments' loads are
+// issued in batches.
+constexpr int kJoinThreads = 128;
+template <int DK>
+__global__ void __launch_bounds__(kJoinThreads) packed_join_kernel(const PackedTcParams a, int quads) {
+  const PackedParams& p = a.p;
+  const int seq = blockIdx.x / quads, head = blockIdx.y;
+  int begin, end;
+  prompt_bounds(p.starts, seq, p.tokens, begin, end);
+  const int segs = prompt_segments(begin, end, a.seg);
+  const size_t tile = static_cast<size_t>(p.dv) * DK;
+  const size_t e = 4 * (static_cast<size_t>(blockIdx.x % quads) * kJoinThreads + threadIdx.x);
+  if (segs < 2 || e >= tile) return;
+  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.S0 != nullptr)
+    S = *reinterpret_cast<const float4*>(p.S0 + (static_cast<size_t>(seq) * p.heads + head) * tile + e);
+  const size_t first = static_cast<size_t>(begin / a.seg) * p.heads + head;
+  constexpr int N = 8;
+  for (int k0 = 0; k0 < segs - 1; k0 += N) {
+    float4 v[N];
+    float d[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const size_t at = first + static_cast<size_t>(min(k0 + i, segs - 2)) * p.heads;
+      v[i] = *reinterpret_cast<const float4*>(a.states + at * tile + e);
+      d[i] = a.decays[at];
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (k0 + i >= segs - 1) break;
+      S.x = __fmaf_rn(S.x, d[i], v[i].x);
+      S.y = __fmaf_rn(S.y, d[i], v[i].y);
+      S.z = __fmaf_rn(S.z, d[i], v[i].z);
+      S.w = __fmaf_rn(S.w, d[i], v[i].w);
+      *reinterpret_cast<float4*>(a.states + (first + static_cast<size_t>(k0 + i) * p.heads) * tile + e) = S;
+    }
+  }
 }
 
 }  // namespace qs
