@@ -35,11 +35,17 @@
 //
 // Warps: 0 loads q, k, v by TMA (128-byte swizzle, a ring of stages); 1
 // issues the contractions; 2 turns alpha and beta into the chunk's factors; 3
-// holds the tensor memory; 4-7 form P from the scores and write the outputs;
-// 8-15 form W and own the state (each of the two warpgroups half of W's
-// tokens and half of S's columns).  All hand-offs are mbarriers; every wait
-// is bounded, and on a timeout the CTA counts it, waits for its copies,
+// holds the tensor memory; 4-7 form P from the scores; 8-11 write the
+// outputs; 12-19 form W and own the state (each of the two warpgroups half of
+// W's tokens and half of S's columns).  All hand-offs are mbarriers; every
+// wait is bounded, and on a timeout the CTA counts it, waits for its copies,
 // frees its tensor memory and returns.
+//
+// What bounds it.  A chunk of 128 x 128 costs the tensor core about 1250
+// cycles (measured: 65 for each of KV's 8 steps, 33 for each of the 16 of O1
+// and the scores, 49 for each of O2's 4).  The other roles run once through
+// their code for every chunk, so instruction fetch and latency bound them,
+// not issue slots: their loops are rolled, 16 columns or tokens a turn.
 #pragma once
 
 #include <cuda.h>
@@ -50,7 +56,7 @@
 
 namespace qs {
 
-constexpr int kPtThreads = 512;
+constexpr int kPtThreads = 640;
 constexpr int kPtChunk = 64;
 // tensor-memory columns
 constexpr uint32_t kPtColScore = 0, kPtColO1 = 64, kPtColO2 = 128, kPtColKV = 192, kPtColS = 320, kPtColW = 384;
@@ -153,16 +159,19 @@ __device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
-// The wait proper, out of line: false once it, or another wait of the CTA
+// Wait for that phase; false once this wait, or another of the CTA's
 // (`failed`), gave up.
-static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* failed) {
-  for (int round = 0; round < 256; ++round) {
-    for (int i = 0; i < 1024; ++i)
-      if (mbar_done(bar, parity)) return true;
-    if (*failed) return false;
+constexpr uint32_t kPtPolls = 1u << 18;
+__device__ __forceinline__ bool mbar_wait_or_fail(uint32_t bar, uint32_t parity, volatile uint32_t* failed) {
+  uint32_t polls = 0;
+#pragma unroll 1
+  while (!mbar_done(bar, parity)) {
+    if ((++polls & 1023u) == 0 && (polls >= kPtPolls || *failed)) {
+      *failed = 1;
+      return false;
+    }
   }
-  *failed = 1;
-  return false;
+  return true;
 }
 
 // The issuing instructions are predicated rather than branched around, which
@@ -206,17 +215,12 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
-// 16 lanes x 64 columns over all 32 threads: registers 4j .. 4j+3 are row
+// 16 lanes x 16 columns over all 32 threads: registers 4j .. 4j+3 are row
 // T/4 (two columns 8j + 2 (T%4)) and row T/4 + 8 (the same columns).
-__device__ __forceinline__ void tm_ld_16x64(uint32_t addr, float (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
-        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
-        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-      : "r"(addr));
+__device__ __forceinline__ void tm_ld_16x16(uint32_t addr, float (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+               : "r"(addr));
 }
 __device__ __forceinline__ void tm_st16u(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -226,12 +230,11 @@ __device__ __forceinline__ void tm_st16u(uint32_t addr, const uint32_t (&r)[16])
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-
-// 16 lanes x 16 columns from all 32 threads: registers 2j and 2j + 1 are
+// 16 lanes x 8 columns from all 32 threads: registers 2j and 2j + 1 are
 // column 4j + T%4 of rows T/4 and T/4 + 8.
-__device__ __forceinline__ void tm_st_16x16(uint32_t addr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+__device__ __forceinline__ void tm_st_16x8(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
                : "memory");
 }
 // Four 8 x 8 matrices of 16-bit elements, transposed: thread T holds elements
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       bar_init(bar(B::kFull + s), 1);
       bar_init(bar(B::kEmpty + s), outputs ? 4 + 8 : 1 + 8);  // the outputs' warps, or the contractions; W's warps
       bar_init(bar(B::kGateFull + s), 1);
-      bar_init(bar(B::kGateFree + s), outputs ? 4 + 8 : 8);  // its readers
+      bar_init(bar(B::kGateFree + s), outputs ? 4 + 4 + 8 : 8);  // its readers
     }
     bar_init(bar(B::kScFull), 1);
     bar_init(bar(B::kScFree), 4);
@@ -343,13 +346,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   // `wait` is for one thread, `wait_all` for a whole warp.
   auto wait = [&](int b, int n) -> bool {
     const uint32_t addr = bar(b), parity = static_cast<uint32_t>(n) & 1u;
-    return n < 0 || mbar_done(addr, parity) || mbar_wait_long(addr, parity, failed);
+    return n < 0 || mbar_wait_or_fail(addr, parity, failed);
   };
   auto wait_all = [&](int b, int n) -> bool {
     if (n < 0) return true;
     const uint32_t addr = bar(b), parity = static_cast<uint32_t>(n) & 1u;
-    if (__all_sync(0xffffffffu, mbar_done(addr, parity))) return true;
-    return __all_sync(0xffffffffu, mbar_wait_long(addr, parity, failed));
+    return __all_sync(0xffffffffu, mbar_wait_or_fail(addr, parity, failed));
   };
   // The warp's work so far is visible to whoever waits for this arrival.
   auto signal = [&](int b) {
@@ -418,199 +420,216 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   };
   const int irow = tc_row<MDV>(qd, lane);  // row of S of this lane
 
+  // Registers: 5 warpgroups of 96 at launch (480 a thread slot); the state's
+  // two take 136 each, the others give up what they do not need: 64 + 64 + 80 +
+  // 2 * 136 = 480.
   bool ok = true;
   int g = 0;  // chunks so far, over all items of this CTA
-  if (warp == 0) {
-    // ---- loads
-    if (lane == 0) {
-      for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-        const Item x = item_at(it);
-        for (int c = 0; ok && c < x.chunks; ++c, ++g) {
-          const int st = g % NST;
-          if (!(ok = wait(B::kEmpty + st, g / NST - 1))) break;
-          const uint32_t s = base + st * L::kStage, f = bar(B::kFull + st);
-          expect_tx(f, (outputs ? L::kStage : L::kStage - L::kK));
-          const int t = x.begin + c * C;
-          for (int i = 0; i < DK / 64; ++i) {
-            if (outputs) tma_load3(s + L::kQ + i * L::kPanel, &mq, 64 * i, x.head / p.share, t, f);
-            tma_load3(s + L::kK + i * L::kPanel, &mk, 64 * i, x.head / p.share, t, f);
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 0) {
+      // ---- loads
+      if (lane == 0) {
+        for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+          const Item x = item_at(it);
+          for (int c = 0; ok && c < x.chunks; ++c, ++g) {
+            const int st = g % NST;
+            if (!(ok = wait(B::kEmpty + st, g / NST - 1))) break;
+            const uint32_t s = base + st * L::kStage, f = bar(B::kFull + st);
+            expect_tx(f, (outputs ? L::kStage : L::kStage - L::kK));
+            const int t = x.begin + c * C;
+            for (int i = 0; i < DK / 64; ++i) {
+              if (outputs) tma_load3(s + L::kQ + i * L::kPanel, &mq, 64 * i, x.head / p.share, t, f);
+              tma_load3(s + L::kK + i * L::kPanel, &mk, 64 * i, x.head / p.share, t, f);
+            }
+            for (int i = 0; i < MDV / 64; ++i)
+              tma_load3(s + L::kV + i * L::kPanel, &mv, x.blk * MDV + 64 * i, x.head, t, f);
           }
-          for (int i = 0; i < MDV / 64; ++i)
-            tma_load3(s + L::kV + i * L::kPanel, &mv, x.blk * MDV + 64 * i, x.head, t, f);
         }
+        // after a timeout: the copies in flight land before the CTA leaves
+        if (!ok)
+          for (int j = max(0, g - NST); j < g; ++j) mbar_wait(bar(B::kFull + j % NST), (j / NST) & 1, 1 << 16);
       }
-      // after a timeout: the copies in flight land before the CTA leaves
-      if (!ok)
-        for (int j = max(0, g - NST); j < g; ++j) mbar_wait(bar(B::kFull + j % NST), (j / NST) & 1, 1 << 16);
-    }
-  } else if (warp == 1) {
-    // ---- contractions: KV(g), O1(g), scores(g + 1), O2(g).  The whole warp
-    // runs the loop, so that addresses stay uniform; one lane issues.
-    constexpr uint32_t id_sc = idesc<E>(C, C, false, false), id_kv = idesc<E>(MDV, DK, false, true),
-                       id_o1 = idesc<E>(MDV, C, false, false), id_o2 = idesc<E>(MDV, C, true, false);
-    // descriptors of stage 0; a byte offset adds a sixteenth of itself
-    const uint64_t dq = desc128(base + L::kQ, 16), dk = desc128(base + L::kK, 16),
-                   dkt = desc128(base + L::kK, L::kPanel), dv = desc128(base + L::kV, L::kPanel),
-                   dp = desc128(base + L::kP, 16);
-    const uint32_t lead = elect_one();
-    auto scores = [&](int n) -> bool {
-      const uint32_t s = (n % NST) * (L::kStage / 16);
-      if (!wait_all(B::kFull + n % NST, n / NST) || !wait_all(B::kScFree, n - 1)) return false;
-      fence_after();
-#pragma unroll
-      for (int k = 0; k < DK / 16; ++k) {
-        const uint32_t off = s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16;
-        mma16_ss(tm + kPtColScore, dq + off, dk + off, id_sc, k > 0, lead);
-      }
-      commit_if(bar(B::kScFull), lead);
-      return true;
-    };
-    int total = 0;
-    for (int it = blockIdx.x; it < a.items; it += gridDim.x) total += item_at(it).chunks;
-    if (outputs && total > 0) ok = scores(0);
-#pragma unroll 1
-    for (; ok && g < total; ++g) {
-      const int st = g % NST;
-      const uint32_t s = st * (L::kStage / 16);
-      // W's warps have waited for this stage's loads; so have the scores
-      if (!(ok = wait_all(B::kWFull + (g & 1), g >> 1) && wait_all(B::kKvFree, g - 1))) break;
-      if (!outputs && !(ok = wait_all(B::kFull + st, g / NST))) break;
-      fence_after();
-      const uint32_t w = tm + kPtColW + 64 * (g & 1);
-#pragma unroll
-      for (int k = 0; k < C / 8; ++k)  // 4 steps of W's value, 4 of its rounding error
-        mma16_ts(tm + kPtColKV, w + 8 * k, dkt + (s + (k % 4) * (2048 / 16)), id_kv, k > 0, lead);
-      commit_if(bar(B::kKvFull), lead);
-      if (outputs) {
-        if (!(ok = wait_all(B::kSFull, g) && wait_all(B::kOFree, g - 1))) break;
+    } else if (warp == 1) {
+      // ---- contractions: KV(g), O1(g), scores(g + 1), O2(g).  The whole warp
+      // runs the loop, so that addresses stay uniform; one lane issues.
+      constexpr uint32_t id_sc = idesc<E>(C, C, false, false), id_kv = idesc<E>(MDV, DK, false, true),
+                         id_o1 = idesc<E>(MDV, C, false, false), id_o2 = idesc<E>(MDV, C, true, false);
+      // descriptors of stage 0; a byte offset adds a sixteenth of itself
+      const uint64_t dq = desc128(base + L::kQ, 16), dk = desc128(base + L::kK, 16),
+                     dkt = desc128(base + L::kK, L::kPanel), dv = desc128(base + L::kV, L::kPanel),
+                     dp = desc128(base + L::kP, 16);
+      const uint32_t lead = elect_one();
+      auto scores = [&](int n) -> bool {
+        const uint32_t s = (n % NST) * (L::kStage / 16);
+        if (!wait_all(B::kFull + n % NST, n / NST) || !wait_all(B::kScFree, n - 1)) return false;
         fence_after();
 #pragma unroll
-        for (int k = 0; k < DK / 16; ++k)
-          mma16_ts(tm + kPtColO1, tm + kPtColS + 8 * k, dq + (s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16), id_o1, k > 0,
-                   lead);
-        commit_if(bar(B::kO1Done), lead);
-        if (g + 1 < total && !(ok = scores(g + 1))) break;
-        if (!(ok = wait_all(B::kPFull + (g & 1), g >> 1))) break;
-        fence_after();
-        const uint32_t pb = (g & 1) * (L::kPanel / 16);
-#pragma unroll
-        for (int k = 0; k < C / 16; ++k)
-          mma16_ss(tm + kPtColO2, dv + (s + k * (2048 / 16)), dp + (pb + 2 * k), id_o2, k > 0, lead);
-        commit_if(bar(B::kOFull), lead);
-        commit_if(bar(B::kPFree + (g & 1)), lead);
-      } else {
-        commit_if(bar(B::kEmpty + st), lead);
-      }
-    }
-  } else if (warp == 2) {
-    // ---- the chunk's factors from alpha and beta, one chunk's loads ahead
-    int it = blockIdx.x, c = 0;
-    Item x{};
-    float a0, a1, b0, b1;
-    auto seek = [&]() {  // the first item from `it` on that has chunks
-      while (it < a.items) {
-        x = item_at(it);
-        if (x.chunks > 0) return;
-        it += gridDim.x;
-      }
-    };
-    auto load = [&]() {
-      const int t = x.begin + c * C, n = x.end - t;
-      const size_t at = static_cast<size_t>(t + lane) * p.heads + x.head, at1 = at + static_cast<size_t>(32) * p.heads;
-      a0 = lane < n ? __ldg(p.alpha + at) : 1.0f;
-      b0 = lane < n ? __ldg(p.beta + at) : 0.0f;
-      a1 = lane + 32 < n ? __ldg(p.alpha + at1) : 1.0f;
-      b1 = lane + 32 < n ? __ldg(p.beta + at1) : 0.0f;
-    };
-    seek();
-    if (it < a.items) load();
-    while (it < a.items) {
-      const int st = g % NST;
-      const float be0 = b0, be1 = b1;
-      const bool z0 = a0 < kPtReset, z1 = a1 < kPtReset;
-      double x0 = z0 ? 0.0 : static_cast<double>(log2f(a0)), x1 = z1 ? 0.0 : static_cast<double>(log2f(a1));
-      if (++c == x.chunks) {
-        c = 0;
-        it += gridDim.x;
-        seek();
-      }
-      if (it < a.items) load();
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const double y0 = __shfl_up_sync(0xffffffffu, x0, d), y1 = __shfl_up_sync(0xffffffffu, x1, d);
-        if (lane >= d) {
-          x0 += y0;
-          x1 += y1;
+        for (int k = 0; k < DK / 16; ++k) {
+          const uint32_t off = s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16;
+          mma16_ss(tm + kPtColScore, dq + off, dk + off, id_sc, k > 0, lead);
         }
-      }
-      x1 += __shfl_sync(0xffffffffu, x0, 31);
-      const double gc = __shfl_sync(0xffffffffu, x1, 31);
-      // the last reset at or before a token: what lies before it is forgotten
-      const uint32_t m0 = __ballot_sync(0xffffffffu, z0), m1 = __ballot_sync(0xffffffffu, z1);
-      const uint32_t le = 0xffffffffu >> (31 - lane);
-      const int r0 = (m0 & le) ? 31 - __clz(m0 & le) : -1;
-      const int r31 = m0 ? 31 - __clz(m0) : -1;
-      const int r1 = (m1 & le) ? 63 - __clz(m1 & le) : r31;
-      const int rc = m1 ? 63 - __clz(m1) : r31;
-      if (!(ok = wait_all(B::kGateFree + st, g / NST - 1))) break;
-      float* f = reinterpret_cast<float*>(sm + L::kGate + st * L::kGateSlot);
-      int* first = reinterpret_cast<int*>(f + Gate::kFirst);
-      auto put = [&](int t, double x, float be, int r) {
-        const double whole = rint(x);
-        f[Gate::kInt + t] = static_cast<float>(whole);
-        f[Gate::kFrac + t] = static_cast<float>(x - whole);
-        f[Gate::kBeta + t] = be;
-        f[Gate::kW + t] = t >= rc ? be * ex2(static_cast<float>(gc - x)) : 0.0f;
-        f[Gate::kDecay + t] = r < 0 ? exp2f(static_cast<float>(x)) : 0.0f;
-        first[t] = max(r, 0);
+        commit_if(bar(B::kScFull), lead);
+        return true;
       };
-      put(lane, x0, be0, r0);
-      put(lane + 32, x1, be1, r1);
-      if (lane == 0) f[Gate::kLast] = rc < 0 ? exp2f(static_cast<float>(gc)) : 0.0f;
-      signal(B::kGateFull + st);
-      ++g;
+      int total = 0;
+      for (int it = blockIdx.x; it < a.items; it += gridDim.x) total += item_at(it).chunks;
+      if (outputs && total > 0) ok = scores(0);
+#pragma unroll 1
+      for (; ok && g < total; ++g) {
+        const int st = g % NST;
+        const uint32_t s = st * (L::kStage / 16);
+        // W's warps have waited for this stage's loads; so have the scores
+        if (!(ok = wait_all(B::kWFull + (g & 1), g >> 1) && wait_all(B::kKvFree, g - 1))) break;
+        if (!outputs && !(ok = wait_all(B::kFull + st, g / NST))) break;
+        fence_after();
+        const uint32_t w = tm + kPtColW + 64 * (g & 1);
+#pragma unroll
+        for (int k = 0; k < C / 8; ++k)  // 4 steps of W's value, 4 of its rounding error
+          mma16_ts(tm + kPtColKV, w + 8 * k, dkt + (s + (k % 4) * (2048 / 16)), id_kv, k > 0, lead);
+        commit_if(bar(B::kKvFull), lead);
+        if (outputs) {
+          if (!(ok = wait_all(B::kSFull, g) && wait_all(B::kOFree, g - 1))) break;
+          fence_after();
+#pragma unroll
+          for (int k = 0; k < DK / 16; ++k)
+            mma16_ts(tm + kPtColO1, tm + kPtColS + 8 * k, dq + (s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16), id_o1, k > 0,
+                     lead);
+          commit_if(bar(B::kO1Done), lead);
+          if (g + 1 < total && !(ok = scores(g + 1))) break;
+          if (!(ok = wait_all(B::kPFull + (g & 1), g >> 1))) break;
+          fence_after();
+          const uint32_t pb = (g & 1) * (L::kPanel / 16);
+#pragma unroll
+          for (int k = 0; k < C / 16; ++k)
+            mma16_ss(tm + kPtColO2, dv + (s + k * (2048 / 16)), dp + (pb + 2 * k), id_o2, k > 0, lead);
+          commit_if(bar(B::kOFull), lead);
+          commit_if(bar(B::kPFree + (g & 1)), lead);
+        } else {
+          commit_if(bar(B::kEmpty + st), lead);
+        }
+      }
+    } else if (warp == 2) {
+      // ---- the chunk's factors from alpha and beta, two chunks' loads ahead
+      struct Raw {
+        float a0, a1, b0, b1;
+      };
+      int it = blockIdx.x, c = 0, left = 0;  // the place of the next load; `left`: chunks loaded and not used
+      Item x{};
+      auto seek = [&]() {  // the first item from `it` on that has chunks
+        for (; it < a.items; it += gridDim.x) {
+          x = item_at(it);
+          if (x.chunks > 0) return;
+        }
+      };
+      auto load = [&]() -> Raw {
+        Raw r{1.0f, 1.0f, 0.0f, 0.0f};
+        if (it >= a.items) return r;
+        const int t = x.begin + c * C, n = x.end - t;
+        const size_t at = static_cast<size_t>(t + lane) * p.heads + x.head, at1 = at + static_cast<size_t>(32) * p.heads;
+        if (lane < n) r.a0 = __ldg(p.alpha + at), r.b0 = __ldg(p.beta + at);
+        if (lane + 32 < n) r.a1 = __ldg(p.alpha + at1), r.b1 = __ldg(p.beta + at1);
+        ++left;
+        if (++c == x.chunks) {
+          c = 0;
+          it += gridDim.x;
+          seek();
+        }
+        return r;
+      };
+      seek();
+      Raw now = load(), next = load();
+      while (left > 0) {
+        const int st = g % NST;
+        const float be0 = now.b0, be1 = now.b1;
+        const bool z0 = now.a0 < kPtReset, z1 = now.a1 < kPtReset;
+        double x0 = z0 ? 0.0 : static_cast<double>(log2f(now.a0)), x1 = z1 ? 0.0 : static_cast<double>(log2f(now.a1));
+        now = next;
+        next = load();
+        --left;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const double y0 = __shfl_up_sync(0xffffffffu, x0, d), y1 = __shfl_up_sync(0xffffffffu, x1, d);
+          if (lane >= d) {
+            x0 += y0;
+            x1 += y1;
+          }
+        }
+        x1 += __shfl_sync(0xffffffffu, x0, 31);
+        const double gc = __shfl_sync(0xffffffffu, x1, 31);
+        // the last reset at or before a token: what lies before it is forgotten
+        const uint32_t m0 = __ballot_sync(0xffffffffu, z0), m1 = __ballot_sync(0xffffffffu, z1);
+        const uint32_t le = 0xffffffffu >> (31 - lane);
+        const int r0 = (m0 & le) ? 31 - __clz(m0 & le) : -1;
+        const int r31 = m0 ? 31 - __clz(m0) : -1;
+        const int r1 = (m1 & le) ? 63 - __clz(m1 & le) : r31;
+        const int rc = m1 ? 63 - __clz(m1) : r31;
+        if (!(ok = wait_all(B::kGateFree + st, g / NST - 1))) break;
+        float* f = reinterpret_cast<float*>(sm + L::kGate + st * L::kGateSlot);
+        int* first = reinterpret_cast<int*>(f + Gate::kFirst);
+        auto put = [&](int t, double x, float be, int r) {
+          const double whole = rint(x);
+          f[Gate::kInt + t] = static_cast<float>(whole);
+          f[Gate::kFrac + t] = static_cast<float>(x - whole);
+          f[Gate::kBeta + t] = be;
+          f[Gate::kW + t] = t >= rc ? be * ex2(static_cast<float>(gc - x)) : 0.0f;
+          f[Gate::kDecay + t] = r < 0 ? exp2f(static_cast<float>(x)) : 0.0f;
+          first[t] = max(r, 0);
+        };
+        put(lane, x0, be0, r0);
+        put(lane + 32, x1, be1, r1);
+        if (lane == 0) f[Gate::kLast] = rc < 0 ? exp2f(static_cast<float>(gc)) : 0.0f;
+        signal(B::kGateFull + st);
+        ++g;
+      }
     }
-  } else if (warp >= 4 && warp < 8) {
-    // ---- P(g + 1), then the outputs of g
+  } else if (warp < 8) {
+    // ---- P
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (outputs) {
+      const int t0 = 16 * qd + lane / 4, t1 = t0 + 8, cc = 2 * (lane % 4);  // this thread's rows, and columns of 8
       auto form_p = [&](int n) -> bool {
         const int st = n % NST, buf = n & 1;
-        if (!wait_all(B::kGateFull + st, n / NST) || !wait_all(B::kScFull, n)) return false;
+        if (!wait_all(B::kGateFull + st, n / NST) || !wait_all(B::kScFull, n) ||
+            !wait_all(B::kPFree + buf, (n >> 1) - 1))
+          return false;
         fence_after();
-        float r[32];
-        tm_ld_16x64(tw + kPtColScore, r);
-        wait_ld();
-        fence_before();
-        signal(B::kScFree);
         const float* f = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot);
         const int* first = reinterpret_cast<const int*>(f + Gate::kFirst);
-        const int t0 = 16 * qd + lane / 4, t1 = t0 + 8, cc = 2 * (lane % 4);
         const float2 i0 = f2(f[Gate::kInt + t0]), i1 = f2(f[Gate::kInt + t1]);
         const float2 f0 = f2(f[Gate::kFrac + t0]), f1 = f2(f[Gate::kFrac + t1]);
         const int l0 = first[t0], l1 = first[t1];
-        float m0 = 0.0f, m1 = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (j >= 2 * (qd + 1)) continue;  // above the diagonal: P stays zero there
+        const unsigned w0 = t0 - l0, w1 = t1 - l1;
+        // the decayed scores of columns 8j + cc and the next, in place
+        auto decayed = [&](int j, float (&r)[8], int i) {
           const int s = 8 * j + cc;
           auto at = [&](int k) { return *reinterpret_cast<const float2*>(f + k + s); };
           const float2 is = at(Gate::kInt), fs = at(Gate::kFrac), be = at(Gate::kBeta);
           const float2 ni = make_float2(-is.x, -is.y), nf = make_float2(-fs.x, -fs.y);
-          auto two = [&](float& a0, float& a1, float2 it, float2 ft, int l, int t) {
+          auto two = [&](float& a0, float& a1, float2 it, float2 ft, int l, unsigned w) {
             const float2 d = __fadd2_rn(__fadd2_rn(it, ni), __fadd2_rn(ft, nf));
             const float2 y = __fmul2_rn(make_float2(a0, a1), __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), be));
-            a0 = static_cast<unsigned>(s - l) <= static_cast<unsigned>(t - l) ? y.x : 0.0f;
-            a1 = static_cast<unsigned>(s + 1 - l) <= static_cast<unsigned>(t - l) ? y.y : 0.0f;
+            a0 = static_cast<unsigned>(s - l) <= w ? y.x : 0.0f;
+            a1 = static_cast<unsigned>(s + 1 - l) <= w ? y.y : 0.0f;
           };
-          two(r[4 * j], r[4 * j + 1], i0, f0, l0, t0);
-          two(r[4 * j + 2], r[4 * j + 3], i1, f1, l1, t1);
-          if constexpr (HALF) {
-            m0 = fmaxf(m0, fmaxf(fabsf(r[4 * j]), fabsf(r[4 * j + 1])));
-            m1 = fmaxf(m1, fmaxf(fabsf(r[4 * j + 2]), fabsf(r[4 * j + 3])));
-          }
-        }
+          two(r[i], r[i + 1], i0, f0, l0, w0);
+          two(r[i + 2], r[i + 3], i1, f1, l1, w1);
+        };
         float s0 = 1.0f, s1 = 1.0f;
         if constexpr (HALF) {
+          float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll 1
+          for (int q = 0; q <= qd; ++q) {
+            float r[8];
+            tm_ld_16x16(tw + kPtColScore + 16 * q, r);
+            wait_ld();
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              decayed(2 * q + e, r, 4 * e);
+              m0 = fmaxf(m0, fmaxf(fabsf(r[4 * e]), fabsf(r[4 * e + 1])));
+              m1 = fmaxf(m1, fmaxf(fabsf(r[4 * e + 2]), fabsf(r[4 * e + 3])));
+            }
+          }
 #pragma unroll
           for (int d = 1; d < 4; d <<= 1) {
             m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
@@ -625,77 +644,96 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             sp[t1] = k1;
           }
         }
-        if (!wait_all(B::kPFree + buf, (n >> 1) - 1)) return false;
-        unsigned char* pb = sm + L::kP + buf * L::kPanel;
+        // columns right of this warp's diagonal block are never written: zero
+        unsigned char* pb = sm + L::kP + buf * L::kPanel + t0 * 128 + 2 * cc;
+#pragma unroll 1
+        for (int q = 0; q <= qd; ++q) {
+          float r[8];
+          tm_ld_16x16(tw + kPtColScore + 16 * q, r);
+          wait_ld();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (j >= 2 * (qd + 1)) continue;
-          *reinterpret_cast<uint32_t*>(pb + t0 * 128 + ((j ^ (t0 & 7)) << 4) + 2 * cc) =
-              E::narrow2(r[4 * j] * s0, r[4 * j + 1] * s0);
-          *reinterpret_cast<uint32_t*>(pb + t1 * 128 + ((j ^ (t1 & 7)) << 4) + 2 * cc) =
-              E::narrow2(r[4 * j + 2] * s1, r[4 * j + 3] * s1);
+          for (int e = 0; e < 2; ++e) {
+            const int j = 2 * q + e;
+            decayed(j, r, 4 * e);
+            const int at = (j ^ (t0 & 7)) << 4;  // t1 & 7 is the same
+            if constexpr (HALF) {
+              r[4 * e] *= s0;
+              r[4 * e + 1] *= s0;
+              r[4 * e + 2] *= s1;
+              r[4 * e + 3] *= s1;
+            }
+            *reinterpret_cast<uint32_t*>(pb + at) = E::narrow2(r[4 * e], r[4 * e + 1]);
+            *reinterpret_cast<uint32_t*>(pb + 1024 + at) = E::narrow2(r[4 * e + 2], r[4 * e + 3]);
+          }
         }
+        fence_before();
         fence_async_smem();
         signal(B::kPFull + buf);
+        if (lane == 0) {
+          arrive(bar(B::kScFree));
+          arrive(bar(B::kGateFree + st));
+        }
         return true;
       };
+      for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x)
+        for (int c = item_at(it).chunks; ok && c > 0; --c, ++g) ok = form_p(g);
+    }
+  } else if (warp < 12) {
+    // ---- outputs
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (outputs) {
       constexpr int WR = MDV / 4;  // rows of a warp
+      const int m = lane >> 3;     // the matrix whose row address this lane gives to stmatrix
       for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
         const Item x = item_at(it);
-        for (int c = 0; ok && c < x.chunks; ++c, ++g) {
-          if (g == 0 && !(ok = form_p(0))) break;
-          if ((c + 1 < x.chunks || count_behind(it) > 0) && !(ok = form_p(g + 1))) break;
+        const int row = x.blk * MDV + WR * qd;  // the warp's first row
+        for (int c = 0; c < x.chunks; ++c, ++g) {
           if (!(ok = wait_all(B::kOFull, g))) break;
           fence_after();
           const int st = g % NST;
-          const float* eg = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot) + Gate::kDecay;
-          const float* sp = reinterpret_cast<const float*>(sm + L::kScaleP) + 64 * (g & 1);
-          const float* ss = reinterpret_cast<const float*>(sm + L::kScaleS) + 128 * (g & 1) + WR * qd;
+          const float* eg = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot) + Gate::kDecay + 2 * (lane % 4);
+          const float* sp = reinterpret_cast<const float*>(sm + L::kScaleP) + 64 * (g & 1) + 2 * (lane % 4);
+          const float* ss = reinterpret_cast<const float*>(sm + L::kScaleS) + 128 * (g & 1) + WR * qd + lane / 4;
           const int t = x.begin + c * C, n = x.end - t;
           // the contractions are done with q and k: their place holds this
           // warp's outputs [64 tokens][WR rows], swizzled as the store wants
           const uint32_t out = base + st * L::kStage + qd * (C * WR * 2);
 #pragma unroll 1
-          for (int h = 0; h < WR / 16; ++h) {
-            float u[32], y[32];
-            tm_ld_16x64(tw + (static_cast<uint32_t>(16 * h) << 16) + kPtColO1, u);
-            tm_ld_16x64(tw + (static_cast<uint32_t>(16 * h) << 16) + kPtColO2, y);
+          for (int i = 0; i < WR / 16 * 4; ++i) {
+            const int h = i >> 2, q = i & 3;  // 16 rows, 16 tokens
+            const uint32_t from = tw + (static_cast<uint32_t>(16 * h) << 16) + 16 * q;
+            float u[8], y[8];
+            tm_ld_16x16(from + kPtColO1, u);
+            tm_ld_16x16(from + kPtColO2, y);
+            const float sa = HALF ? ss[16 * h] : 1.0f, sb = HALF ? ss[16 * h + 8] : 1.0f;
             wait_ld();
-            if (h == WR / 16 - 1 && !HALF) {
-              fence_before();
-              signal(B::kOFree);
-            }
-            const float sa = HALF ? ss[16 * h + lane / 4] : 1.0f, sb = HALF ? ss[16 * h + 8 + lane / 4] : 1.0f;
-            uint32_t w[16];
+            uint32_t w[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float2 d = *reinterpret_cast<const float2*>(eg + 8 * j + 2 * (lane % 4));
-              float2 ya = make_float2(y[4 * j], y[4 * j + 1]), yb = make_float2(y[4 * j + 2], y[4 * j + 3]);
+            for (int e = 0; e < 2; ++e) {
+              const float2 d = *reinterpret_cast<const float2*>(eg + 16 * q + 8 * e);
+              float2 ya = make_float2(y[4 * e], y[4 * e + 1]), yb = make_float2(y[4 * e + 2], y[4 * e + 3]);
               float2 da = d, db = d;
               if constexpr (HALF) {
-                const float2 k = *reinterpret_cast<const float2*>(sp + 8 * j + 2 * (lane % 4));
+                const float2 k = *reinterpret_cast<const float2*>(sp + 16 * q + 8 * e);
                 ya = __fmul2_rn(k, ya);
                 yb = __fmul2_rn(k, yb);
                 da = __fmul2_rn(d, f2(sa));
                 db = __fmul2_rn(d, f2(sb));
               }
-              const float2 oa = __ffma2_rn(da, make_float2(u[4 * j], u[4 * j + 1]), ya);
-              const float2 ob = __ffma2_rn(db, make_float2(u[4 * j + 2], u[4 * j + 3]), yb);
-              w[2 * j] = E::narrow2(oa.x, oa.y);
-              w[2 * j + 1] = E::narrow2(ob.x, ob.y);
+              const float2 oa = __ffma2_rn(da, make_float2(u[4 * e], u[4 * e + 1]), ya);
+              const float2 ob = __ffma2_rn(db, make_float2(u[4 * e + 2], u[4 * e + 3]), yb);
+              w[2 * e] = E::narrow2(oa.x, oa.y);
+              w[2 * e + 1] = E::narrow2(ob.x, ob.y);
             }
             // matrices: rows 16h.. and 16h + 8.. of two blocks of 8 tokens
-            const int m = lane >> 3, chunk = 2 * h + (m & 1);
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              const int tt = 8 * (j + (m >> 1)) + (lane & 7);
-              const int sw = WR == 32 ? (tt >> 1) & 3 : (tt >> 2) & 1;
-              stsm4_t(out + tt * (2 * WR) + ((chunk ^ sw) << 4), w[2 * j], w[2 * j + 1], w[2 * j + 2], w[2 * j + 3]);
-            }
+            const int tt = 16 * q + 8 * (m >> 1) + (lane & 7), chunk = 2 * h + (m & 1);
+            const int sw = WR == 32 ? (tt >> 1) & 3 : (tt >> 2) & 1;
+            stsm4_t(out + tt * (2 * WR) + ((chunk ^ sw) << 4), w[0], w[1], w[2], w[3]);
           }
+          fence_before();
           fence_async_smem();
-          __syncwarp();
-          const int row = x.blk * MDV + WR * qd;  // the warp's first row
+          signal(B::kOFree);
+          if (lane == 0) arrive(bar(B::kGateFree + st));
           if (n >= C) {
             if (lane == 0 && row < p.dv) tma_store3(&mo, out, row, x.head, t);
           } else {
@@ -705,6 +743,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (row + 8 * piece < p.dv) {
               T* o = static_cast<T*>(p.o) + static_cast<size_t>(t) * p.o_stride + static_cast<size_t>(x.head) * p.dv + row +
                      8 * piece;
+#pragma unroll 1
               for (int tt = lane / PER; tt < n; tt += 32 / PER) {
                 const int sw = WR == 32 ? (tt >> 1) & 3 : (tt >> 2) & 1;
                 *reinterpret_cast<uint4*>(o + tt * p.o_stride) = *reinterpret_cast<const uint4*>(
@@ -718,17 +757,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
           }
           if (g > 0) signal(B::kEmpty + (g - 1) % NST);
-          if constexpr (HALF) {  // the row scales are read as well
-            fence_before();
-            signal(B::kOFree);
-          }
-          signal(B::kGateFree + st);
         }
       }
     }
-  } else if (warp >= 8) {
+  } else {
     // ---- W(g + 1), then the state behind chunk g
-    const int half = (warp - 8) >> 2;  // which half of W's tokens and of S's columns
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+    const int half = (warp - 12) >> 2;  // which half of W's tokens and of S's columns
     constexpr int SC = DK / 2;
     float2 S[SC / 2];
     int pairs = 0;
@@ -748,54 +783,47 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       if (count < C) {
         // the rows behind the prompt's end belong to others: zeros for the contractions
         const int n16 = (C - count) * 8;
-        for (int i = tid - 256; i < n16 * ((DK + MDV) / 64); i += 256) {
+        for (int i = tid - 384; i < n16 * ((DK + MDV) / 64); i += 256) {
           const int panel = i / n16, j = i % n16;
           *reinterpret_cast<uint4*>(sm + st * L::kStage + L::kK + panel * L::kPanel + (count + j / 8) * 128 +
                                     16 * (j % 8)) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_async_smem();
       }
-      float2 w[4];
-      {
-        const float* f = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot) + Gate::kW + 32 * half;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const float2*>(f + 8 * j + 2 * (lane % 4));
-      }
-      // w v of row half h (16 rows): pairs of tokens, [j][0] row T/4, [j][1] row T/4 + 8
-      auto values = [&](int h, float2 (&x)[4][2]) {
+      const float* wt = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot) + Gate::kW + 32 * half + 2 * (lane % 4);
+      const int m = lane >> 3;  // the matrix whose row address this lane gives to ldmatrix
+      // w v of rows 16h.. and tokens 16q..: pairs of tokens 8j + 2 (T%4) and
+      // the next, [j][0] of row T/4, [j][1] of row T/4 + 8
+      auto values = [&](int h, int q, float2 (&x)[2][2]) {
         const int col = (MDV / 4) * qd + 16 * h;  // first row of S, a column of v
-        const uint32_t panel = s + L::kV + (col >> 6) * L::kPanel + 32 * half * 128;
-        const int m = lane >> 3, chunk = ((col & 63) >> 3) + (m & 1);
-        uint32_t r[4][2];
+        const int t = 32 * half + 16 * q + 8 * (m >> 1) + (lane & 7), chunk = ((col & 63) >> 3) + (m & 1);
+        uint32_t r[2][2];
+        ldsm4_t(s + L::kV + (col >> 6) * L::kPanel + t * 128 + ((chunk ^ (t & 7)) << 4), r[0][0], r[0][1], r[1][0], r[1][1]);
 #pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          const int t = 8 * (j + (m >> 1)) + (lane & 7);
-          ldsm4_t(panel + t * 128 + ((chunk ^ (t & 7)) << 4), r[j][0], r[j][1], r[j + 1][0], r[j + 1][1]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j][0] = __fmul2_rn(w[j], E::widen2(r[j][0]));
-          x[j][1] = __fmul2_rn(w[j], E::widen2(r[j][1]));
-        }
-        if (count < C) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int t = 32 * half + 8 * j + 2 * (lane % 4);
-            if (t >= count) x[j][0].x = x[j][1].x = 0.0f;
-            if (t + 1 >= count) x[j][0].y = x[j][1].y = 0.0f;
+        for (int j = 0; j < 2; ++j) {
+          const float2 w = *reinterpret_cast<const float2*>(wt + 16 * q + 8 * j);
+          x[j][0] = __fmul2_rn(w, E::widen2(r[j][0]));
+          x[j][1] = __fmul2_rn(w, E::widen2(r[j][1]));
+          if (count < C) {
+            const int tt = 32 * half + 16 * q + 8 * j + 2 * (lane % 4);
+            if (tt >= count) x[j][0].x = x[j][1].x = 0.0f;
+            if (tt + 1 >= count) x[j][0].y = x[j][1].y = 0.0f;
           }
         }
       };
       if constexpr (HALF) {
 #pragma unroll 1
         for (int h = 0; h < MDV / 64; ++h) {
-          float2 x[4][2];
-          values(h, x);
           float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            m0 = fmaxf(m0, fmaxf(fabsf(x[j][0].x), fabsf(x[j][0].y)));
-            m1 = fmaxf(m1, fmaxf(fabsf(x[j][1].x), fabsf(x[j][1].y)));
+          for (int q = 0; q < 2; ++q) {
+            float2 x[2][2];
+            values(h, q, x);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              m0 = fmaxf(m0, fmaxf(fabsf(x[j][0].x), fabsf(x[j][0].y)));
+              m1 = fmaxf(m1, fmaxf(fabsf(x[j][1].x), fabsf(x[j][1].y)));
+            }
           }
 #pragma unroll
           for (int d = 1; d < 4; d <<= 1) {
@@ -812,30 +840,31 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       }
       const uint32_t at = tw + kPtColW + 64 * (n & 1) + 16 * half;
 #pragma unroll 1
-      for (int h = 0; h < MDV / 64; ++h) {
-        float2 x[4][2];
-        values(h, x);
+      for (int i = 0; i < MDV / 64 * 2; ++i) {
+        const int h = i >> 1, q = i & 1;
+        float2 x[2][2];
+        values(h, q, x);
         if constexpr (HALF) {
           const int row = (MDV / 4) * qd + 16 * h + lane / 4;
           float back;
           const float u0 = row_scale(worst(n & 3, row), back), u1 = row_scale(worst(n & 3, row + 8), back);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 2; ++j) {
             x[j][0] = __fmul2_rn(x[j][0], f2(u0));
             x[j][1] = __fmul2_rn(x[j][1], f2(u1));
           }
         }
-        uint32_t hi[8], lo[8];
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const float2 v = x[j / 2][j % 2];
           hi[j] = E::narrow2(v.x, v.y);
           const float2 k = E::widen2(hi[j]);
           lo[j] = E::narrow2(v.x - k.x, v.y - k.y);
         }
-        const uint32_t to = at + (static_cast<uint32_t>(16 * h) << 16);
-        tm_st_16x16(to, hi);
-        tm_st_16x16(to + 32, lo);
+        const uint32_t to = at + (static_cast<uint32_t>(16 * h) << 16) + 8 * q;
+        tm_st_16x8(to, hi);
+        tm_st_16x8(to + 32, lo);
       }
       wait_st();
       fence_before();
@@ -875,18 +904,23 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       signal(B::kSFull);
       return true;
     };
+    // this thread's part of a head's state, or null where it has none
+    auto part = [&](const float* state, int blk) {
+      const int row = blk * MDV + irow;
+      return irow >= 0 && row < p.dv && state != nullptr ? const_cast<float*>(state) + static_cast<size_t>(row) * DK + SC * half
+                                                         : nullptr;
+    };
     for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-      const Item x = item_at(it);
-      const int row = x.blk * MDV + irow;
-      const bool live = irow >= 0 && row < p.dv;
-      const size_t at = static_cast<size_t>(live ? row : 0) * DK + SC * half;
-      float decay = 1.0f;  // of the item so far
-      if (x.to != nullptr || x.chunks > 0) {
-        if (live && x.from != nullptr) {
+      int tokens;
+      {
+        const Item x = item_at(it);
+        tokens = x.end - x.begin;
+        const float* from = part(x.from, x.blk);
+        if (from != nullptr) {
 #pragma unroll
           for (int j = 0; j < SC; j += 8) {
             float v[8];
-            load8<F32>(v, x.from + at + j);
+            load8<F32>(v, from + j);
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[j / 2 + i] = make_float2(v[2 * i], v[2 * i + 1]);
           }
@@ -895,12 +929,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           for (int j = 0; j < SC / 2; ++j) S[j] = f2(0.0f);
         }
       }
-      if (x.chunks > 0) {
-        if (g == 0) ok = form_w(0, x.end - x.begin);
+      float decay = 1.0f;  // of the item so far
+      if (tokens > 0) {
+        if (g == 0) ok = form_w(0, tokens);
         if (ok && outputs) ok = put_state(g);
       }
-      for (int c = 0; ok && c < x.chunks; ++c, ++g) {
-        const int count = c + 1 < x.chunks ? x.end - x.begin - (c + 1) * C : count_behind(it);
+      for (; ok && tokens > 0; tokens -= C, ++g) {
+        const int count = tokens > C ? tokens - C : count_behind(it);
         if (count > 0) ok = form_w(g + 1, count);
         if (!ok || !(ok = wait_all(B::kKvFull, g))) break;
         fence_after();
@@ -926,9 +961,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             S[8 * q + e] = __ffma2_rn(S[8 * q + e], f2(gamma), v);
           }
         }
-        if (outputs && c + 1 < x.chunks) ok = put_state(g + 1);
+        if (outputs && tokens > C) ok = put_state(g + 1);
       }
-      if (ok && live && x.to != nullptr) {
+      if (!ok) break;
+      const Item x = item_at(it);
+      float* to = part(x.to, x.blk);
+      if (to != nullptr) {
 #pragma unroll
         for (int j = 0; j < SC; j += 8) {
           float v[8];
@@ -937,15 +975,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             v[2 * i] = S[j / 2 + i].x;
             v[2 * i + 1] = S[j / 2 + i].y;
           }
-          store8<F32>(x.to + at + j, v);
+          store8<F32>(to + j, v);
         }
       }
-      if (ok && x.decay != nullptr && tid == 256 && x.blk == 0) *x.decay = decay;
+      if (x.decay != nullptr && tid == 384 && x.blk == 0) *x.decay = decay;
     }
   }
 
   // the outputs' stores have read shared memory before it goes
-  if (warp >= 4 && warp < 8 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  if (warp >= 8 && warp < 12 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncwarp();
   if (!ok) *failed = 1;
   __syncthreads();
