@@ -104,9 +104,18 @@ struct PtLayout {
 
 // A chunk's factors, in floats from its gate slot: the integers and
 // fractions of G, beta, W's weights 2^{G_C - G} beta, 2^G, the first token
-// that a token still sees (int), and 2^{G_C}.
+// that a token still sees (int), and what the chunk is (Chunk).
 struct Gate {
-  static constexpr int kInt = 0, kFrac = 64, kBeta = 128, kW = 192, kDecay = 256, kFirst = 320, kLast = 384;
+  static constexpr int kInt = 0, kFrac = 64, kBeta = 128, kW = 192, kDecay = 256, kFirst = 320, kChunk = 384;
+};
+struct Chunk {
+  const float* from;  // first chunk of an item: the head's state before it (null: zeros)
+  float* to;          // last chunk of an item: where the state goes (null: nowhere)
+  float* decay;       // last chunk of an item: where the item's whole decay goes (null: nowhere)
+  float last;         // 2^{G_C}
+  int t, n;           // first token, tokens (0: the state alone); n < 0: no more chunks
+  int head, row;      // head, first row of S
+  int first, final;   // of its item
 };
 
 // mbarriers, 8 bytes each
@@ -140,12 +149,12 @@ __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lbo) {
 }
 
 // One lane of a converged warp.
-__device__ __forceinline__ uint32_t elect_one() {
+__device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(p));
-  return p;
+  return p != 0;
 }
 
 // One look at the phase of the given parity.
@@ -174,27 +183,18 @@ __device__ __forceinline__ bool mbar_wait_or_fail(uint32_t bar, uint32_t parity,
   return true;
 }
 
-// The issuing instructions are predicated rather than branched around, which
-// keeps the warp together and their operands uniform.
-__device__ __forceinline__ void mma16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t lead) {
+__device__ __forceinline__ void mma16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(lead)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t lead) {
+__device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void commit_if(uint32_t mbar, uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(mbar),
-      "r"(lead)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
 
@@ -341,29 +341,28 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   constexpr uint32_t tm = 0;
   const uint32_t tw = tm + (static_cast<uint32_t>(32 * qd) << 16);  // this warp's lanes
 
-  // Wait for completion number n of a barrier (the caller's count; n < 0:
-  // nothing to wait for).  False once this wait or another gave up.
-  // `wait` is for one thread, `wait_all` for a whole warp.
+  // Completion number n of a barrier (n < 0 is complete from the start);
+  // `wait` for one thread, `wait_all` for a whole warp.  False once this wait
+  // or another gave up.
   auto wait = [&](int b, int n) -> bool {
-    const uint32_t addr = bar(b), parity = static_cast<uint32_t>(n) & 1u;
-    return n < 0 || mbar_wait_or_fail(addr, parity, failed);
+    return mbar_wait_or_fail(bar(b), static_cast<uint32_t>(n) & 1u, failed);
   };
-  auto wait_all = [&](int b, int n) -> bool {
-    if (n < 0) return true;
-    const uint32_t addr = bar(b), parity = static_cast<uint32_t>(n) & 1u;
-    return __all_sync(0xffffffffu, mbar_wait_or_fail(addr, parity, failed));
-  };
+  auto wait_all = [&](int b, int n) -> bool { return __all_sync(0xffffffffu, wait(b, n)); };
   // The warp's work so far is visible to whoever waits for this arrival.
   auto signal = [&](int b) {
     __syncwarp();
     if (lane == 0) arrive(bar(b));
   };
+  auto gate_of = [&](int n) { return reinterpret_cast<float*>(sm + L::kGate + (n % NST) * L::kGateSlot); };
+  auto chunk_of = [&](int n) -> const volatile Chunk& {
+    return *reinterpret_cast<const volatile Chunk*>(gate_of(n) + Gate::kChunk);
+  };
 
   struct Item {
     int head, blk, begin, end, chunks;
-    const float* from;  // the head's state before the item (null: zeros)
-    float* to;          // and where it goes after it (null: nowhere)
-    float* decay;       // where the item's whole decay goes (null: nowhere)
+    const float* from;  // as in Chunk
+    float* to;
+    float* decay;
   };
   auto item_at = [&](int it) {
     Item x;
@@ -376,6 +375,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const int unit = seq;
       auto first = [&](int i) { return min(max(__ldg(p.starts + i), 0), p.tokens) / a.seg + i; };
       int lo = 0, hi = a.sequences - 1;
+#pragma unroll 1
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (first(mid) <= unit) lo = mid; else hi = mid - 1;
@@ -388,35 +388,28 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     x.from = p.S0 == nullptr ? nullptr : p.S0 + at;
     x.to = p.S1 + at;
     x.decay = nullptr;
+    bool work = true;
     if (a.seg > 0) {
       const int segs = prompt_segments(x.begin, x.end, a.seg);
       auto stored = [&](int k) { return static_cast<size_t>((x.begin + k * a.seg) / a.seg) * p.heads + x.head; };
-      const bool last = seg >= segs - 1;
-      if (seg < 0 || seg >= segs || (a.local && last)) {
-        x.end = x.begin;
-        x.to = nullptr;
-      } else if (a.local) {
-        x.from = nullptr;
-        x.to = a.states + stored(seg) * tile;
-        x.decay = a.decays + stored(seg);
-      } else {
-        if (seg > 0) x.from = a.states + stored(seg - 1) * tile;
-        if (!last) x.to = nullptr;
+      const bool final = seg >= segs - 1;
+      work = seg >= 0 && seg < segs && !(a.local && final);
+      if (work) {
+        if (a.local) {
+          x.from = nullptr;
+          x.to = a.states + stored(seg) * tile;
+          x.decay = a.decays + stored(seg);
+        } else {
+          if (seg > 0) x.from = a.states + stored(seg - 1) * tile;
+          if (!final) x.to = nullptr;
+        }
+        x.begin += seg * a.seg;
+        if (!final) x.end = x.begin + a.seg;
       }
-      if (seg > 0) x.begin += seg * a.seg;
-      if (!last) x.end = min(x.end, x.begin + a.seg);
-      x.end = max(x.end, x.begin);
     }
-    x.chunks = (x.end - x.begin + C - 1) / C;
+    // an empty prompt is one chunk of no tokens: its state is handed on
+    x.chunks = work ? max((x.end - x.begin + C - 1) / C, 1) : 0;
     return x;
-  };
-  // Tokens of the CTA's next item behind `it` that has any; 0: none has.
-  auto count_behind = [&](int it) {
-    for (it += gridDim.x; it < a.items; it += gridDim.x) {
-      const Item x = item_at(it);
-      if (x.chunks > 0) return x.end - x.begin;
-    }
-    return 0;
   };
   const int irow = tc_row<MDV>(qd, lane);  // row of S of this lane
 
@@ -430,18 +423,22 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     if (warp == 0) {
       // ---- loads
       if (lane == 0) {
+#pragma unroll 1
         for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
           const Item x = item_at(it);
-          for (int c = 0; ok && c < x.chunks; ++c, ++g) {
+#pragma unroll 1
+          for (int c = 0; c < x.chunks; ++c, ++g) {
             const int st = g % NST;
             if (!(ok = wait(B::kEmpty + st, g / NST - 1))) break;
             const uint32_t s = base + st * L::kStage, f = bar(B::kFull + st);
             expect_tx(f, (outputs ? L::kStage : L::kStage - L::kK));
             const int t = x.begin + c * C;
+#pragma unroll
             for (int i = 0; i < DK / 64; ++i) {
               if (outputs) tma_load3(s + L::kQ + i * L::kPanel, &mq, 64 * i, x.head / p.share, t, f);
               tma_load3(s + L::kK + i * L::kPanel, &mk, 64 * i, x.head / p.share, t, f);
             }
+#pragma unroll
             for (int i = 0; i < MDV / 64; ++i)
               tma_load3(s + L::kV + i * L::kPanel, &mv, x.blk * MDV + 64 * i, x.head, t, f);
           }
@@ -459,95 +456,119 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const uint64_t dq = desc128(base + L::kQ, 16), dk = desc128(base + L::kK, 16),
                      dkt = desc128(base + L::kK, L::kPanel), dv = desc128(base + L::kV, L::kPanel),
                      dp = desc128(base + L::kP, 16);
-      const uint32_t lead = elect_one();
-      auto scores = [&](int n) -> bool {
-        const uint32_t s = (n % NST) * (L::kStage / 16);
-        if (!wait_all(B::kFull + n % NST, n / NST) || !wait_all(B::kScFree, n - 1)) return false;
-        fence_after();
-#pragma unroll
-        for (int k = 0; k < DK / 16; ++k) {
-          const uint32_t off = s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16;
-          mma16_ss(tm + kPtColScore, dq + off, dk + off, id_sc, k > 0, lead);
-        }
-        commit_if(bar(B::kScFull), lead);
-        return true;
+      // The gate slot of chunk n is full: is there one?
+      auto exists = [&](int n) -> bool {
+        if (!(ok = wait_all(B::kGateFull + n % NST, n / NST))) return false;
+        return chunk_of(n).n >= 0;
       };
-      int total = 0;
-      for (int it = blockIdx.x; it < a.items; it += gridDim.x) total += item_at(it).chunks;
-      if (outputs && total > 0) ok = scores(0);
+      bool more = exists(0);
+      // scores(0) starts the pipeline; from then on, scores(g + 1) follow O1(g)
+      int n = outputs ? 0 : 1;
 #pragma unroll 1
-      for (; ok && g < total; ++g) {
-        const int st = g % NST;
-        const uint32_t s = st * (L::kStage / 16);
-        // W's warps have waited for this stage's loads; so have the scores
-        if (!(ok = wait_all(B::kWFull + (g & 1), g >> 1) && wait_all(B::kKvFree, g - 1))) break;
-        if (!outputs && !(ok = wait_all(B::kFull + st, g / NST))) break;
-        fence_after();
-        const uint32_t w = tm + kPtColW + 64 * (g & 1);
-#pragma unroll
-        for (int k = 0; k < C / 8; ++k)  // 4 steps of W's value, 4 of its rounding error
-          mma16_ts(tm + kPtColKV, w + 8 * k, dkt + (s + (k % 4) * (2048 / 16)), id_kv, k > 0, lead);
-        commit_if(bar(B::kKvFull), lead);
-        if (outputs) {
-          if (!(ok = wait_all(B::kSFull, g) && wait_all(B::kOFree, g - 1))) break;
+      while (ok && more) {
+        if (n > g) {  // chunk g's own contractions
+          const uint32_t s = (g % NST) * (L::kStage / 16);
+          // W's warps have waited for this stage's loads; so have the scores
+          if (!(ok = wait_all(B::kWFull + (g & 1), g >> 1) && wait_all(B::kKvFree, g - 1))) break;
+          if (!outputs && !(ok = wait_all(B::kFull + g % NST, g / NST))) break;
           fence_after();
+          if (elect_one()) {
+            const uint32_t w = tm + kPtColW + 64 * (g & 1);
 #pragma unroll
-          for (int k = 0; k < DK / 16; ++k)
-            mma16_ts(tm + kPtColO1, tm + kPtColS + 8 * k, dq + (s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16), id_o1, k > 0,
-                     lead);
-          commit_if(bar(B::kO1Done), lead);
-          if (g + 1 < total && !(ok = scores(g + 1))) break;
-          if (!(ok = wait_all(B::kPFull + (g & 1), g >> 1))) break;
-          fence_after();
-          const uint32_t pb = (g & 1) * (L::kPanel / 16);
+            for (int k = 0; k < C / 8; ++k)  // 4 steps of W's value, 4 of its rounding error
+              mma16_ts(tm + kPtColKV, w + 8 * k, dkt + (s + (k % 4) * (2048 / 16)), id_kv, k > 0);
+            mma_commit(bar(B::kKvFull));
+            if (!outputs) mma_commit(bar(B::kEmpty + g % NST));
+          }
+          __syncwarp();
+          more = exists(g + 1);
+          if (!ok) break;
+          if (outputs) {
+            if (!(ok = wait_all(B::kSFull, g) && wait_all(B::kOFree, g - 1))) break;
+            fence_after();
+            if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < C / 16; ++k)
-            mma16_ss(tm + kPtColO2, dv + (s + k * (2048 / 16)), dp + (pb + 2 * k), id_o2, k > 0, lead);
-          commit_if(bar(B::kOFull), lead);
-          commit_if(bar(B::kPFree + (g & 1)), lead);
-        } else {
-          commit_if(bar(B::kEmpty + st), lead);
+              for (int k = 0; k < DK / 16; ++k)
+                mma16_ts(tm + kPtColO1, tm + kPtColS + 8 * k, dq + (s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16), id_o1,
+                         k > 0);
+              mma_commit(bar(B::kO1Done));
+            }
+            __syncwarp();
+          }
         }
+        if (outputs && more) {  // scores(n)
+          if (!(ok = wait_all(B::kFull + n % NST, n / NST) && wait_all(B::kScFree, n - 1))) break;
+          fence_after();
+          if (elect_one()) {
+            const uint32_t s = (n % NST) * (L::kStage / 16);
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k) {
+              const uint32_t off = s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16;
+              mma16_ss(tm + kPtColScore, dq + off, dk + off, id_sc, k > 0);
+            }
+            mma_commit(bar(B::kScFull));
+          }
+          __syncwarp();
+        }
+        if (n > g) {
+          if (outputs) {
+            const uint32_t s = (g % NST) * (L::kStage / 16), pb = (g & 1) * (L::kPanel / 16);
+            if (!(ok = wait_all(B::kPFull + (g & 1), g >> 1))) break;
+            fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < C / 16; ++k)
+                mma16_ss(tm + kPtColO2, dv + (s + k * (2048 / 16)), dp + (pb + 2 * k), id_o2, k > 0);
+              mma_commit(bar(B::kOFull));
+              mma_commit(bar(B::kPFree + (g & 1)));
+            }
+            __syncwarp();
+          }
+          ++g;
+        }
+        ++n;
       }
     } else if (warp == 2) {
-      // ---- the chunk's factors from alpha and beta, two chunks' loads ahead
-      struct Raw {
+      // ---- what each chunk is, and its factors from alpha and beta, whose
+      // loads are issued a chunk ahead
+      struct Ahead {
         float a0, a1, b0, b1;
+        Chunk c;
       };
-      int it = blockIdx.x, c = 0, left = 0;  // the place of the next load; `left`: chunks loaded and not used
+      int it = blockIdx.x, c = 0;
       Item x{};
-      auto seek = [&]() {  // the first item from `it` on that has chunks
-        for (; it < a.items; it += gridDim.x) {
-          x = item_at(it);
-          if (x.chunks > 0) return;
-        }
-      };
-      auto load = [&]() -> Raw {
-        Raw r{1.0f, 1.0f, 0.0f, 0.0f};
-        if (it >= a.items) return r;
-        const int t = x.begin + c * C, n = x.end - t;
-        const size_t at = static_cast<size_t>(t + lane) * p.heads + x.head, at1 = at + static_cast<size_t>(32) * p.heads;
-        if (lane < n) r.a0 = __ldg(p.alpha + at), r.b0 = __ldg(p.beta + at);
-        if (lane + 32 < n) r.a1 = __ldg(p.alpha + at1), r.b1 = __ldg(p.beta + at1);
-        ++left;
-        if (++c == x.chunks) {
+      auto load = [&](Ahead& r) {  // the next chunk; n < 0: none
+        if (c == x.chunks) {
           c = 0;
-          it += gridDim.x;
-          seek();
+          for (x.chunks = 0; it < a.items && x.chunks == 0; it += gridDim.x) x = item_at(it);
         }
-        return r;
+        r.a0 = r.a1 = 1.0f;
+        r.b0 = r.b1 = 0.0f;
+        r.c.n = -1;
+        if (x.chunks == 0) return;
+        r.c.t = x.begin + c * C;
+        r.c.n = min(x.end - r.c.t, C);
+        r.c.head = x.head;
+        r.c.row = x.blk * MDV;
+        r.c.first = c == 0;
+        r.c.final = ++c == x.chunks;
+        r.c.from = x.from;
+        r.c.to = x.to;
+        r.c.decay = x.decay;
+        const size_t at = static_cast<size_t>(r.c.t + lane) * p.heads + x.head, at1 = at + static_cast<size_t>(32) * p.heads;
+        if (lane < r.c.n) r.a0 = __ldg(p.alpha + at), r.b0 = __ldg(p.beta + at);
+        if (lane + 32 < r.c.n) r.a1 = __ldg(p.alpha + at1), r.b1 = __ldg(p.beta + at1);
       };
-      seek();
-      Raw now = load(), next = load();
-      while (left > 0) {
-        const int st = g % NST;
-        const float be0 = now.b0, be1 = now.b1;
+      Ahead next;
+      load(next);
+#pragma unroll 1
+      for (bool more = true; more; ++g) {
+        const Ahead now = next;
+        more = now.c.n >= 0;
+        if (more) load(next);
         const bool z0 = now.a0 < kPtReset, z1 = now.a1 < kPtReset;
         double x0 = z0 ? 0.0 : static_cast<double>(log2f(now.a0)), x1 = z1 ? 0.0 : static_cast<double>(log2f(now.a1));
-        now = next;
-        next = load();
-        --left;
-#pragma unroll
+#pragma unroll 1
         for (int d = 1; d < 32; d <<= 1) {
           const double y0 = __shfl_up_sync(0xffffffffu, x0, d), y1 = __shfl_up_sync(0xffffffffu, x1, d);
           if (lane >= d) {
@@ -564,8 +585,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int r31 = m0 ? 31 - __clz(m0) : -1;
         const int r1 = (m1 & le) ? 63 - __clz(m1 & le) : r31;
         const int rc = m1 ? 63 - __clz(m1) : r31;
-        if (!(ok = wait_all(B::kGateFree + st, g / NST - 1))) break;
-        float* f = reinterpret_cast<float*>(sm + L::kGate + st * L::kGateSlot);
+        if (!(ok = wait_all(B::kGateFree + g % NST, g / NST - 1))) break;
+        float* f = gate_of(g);
         int* first = reinterpret_cast<int*>(f + Gate::kFirst);
         auto put = [&](int t, double x, float be, int r) {
           const double whole = rint(x);
@@ -576,76 +597,50 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           f[Gate::kDecay + t] = r < 0 ? exp2f(static_cast<float>(x)) : 0.0f;
           first[t] = max(r, 0);
         };
-        put(lane, x0, be0, r0);
-        put(lane + 32, x1, be1, r1);
-        if (lane == 0) f[Gate::kLast] = rc < 0 ? exp2f(static_cast<float>(gc)) : 0.0f;
-        signal(B::kGateFull + st);
-        ++g;
+        put(lane, x0, now.b0, r0);
+        put(lane + 32, x1, now.b1, r1);
+        if (lane == 0) {
+          Chunk k = now.c;
+          k.last = rc < 0 ? exp2f(static_cast<float>(gc)) : 0.0f;
+          *reinterpret_cast<Chunk*>(f + Gate::kChunk) = k;
+        }
+        signal(B::kGateFull + g % NST);
       }
     }
   } else if (warp < 8) {
     // ---- P
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (outputs) {
-      const int t0 = 16 * qd + lane / 4, t1 = t0 + 8, cc = 2 * (lane % 4);  // this thread's rows, and columns of 8
-      auto form_p = [&](int n) -> bool {
-        const int st = n % NST, buf = n & 1;
-        if (!wait_all(B::kGateFull + st, n / NST) || !wait_all(B::kScFull, n) ||
-            !wait_all(B::kPFree + buf, (n >> 1) - 1))
-          return false;
-        fence_after();
-        const float* f = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot);
-        const int* first = reinterpret_cast<const int*>(f + Gate::kFirst);
-        const float2 i0 = f2(f[Gate::kInt + t0]), i1 = f2(f[Gate::kInt + t1]);
-        const float2 f0 = f2(f[Gate::kFrac + t0]), f1 = f2(f[Gate::kFrac + t1]);
-        const int l0 = first[t0], l1 = first[t1];
-        const unsigned w0 = t0 - l0, w1 = t1 - l1;
-        // the decayed scores of columns 8j + cc and the next, in place
-        auto decayed = [&](int j, float (&r)[8], int i) {
-          const int s = 8 * j + cc;
-          auto at = [&](int k) { return *reinterpret_cast<const float2*>(f + k + s); };
-          const float2 is = at(Gate::kInt), fs = at(Gate::kFrac), be = at(Gate::kBeta);
-          const float2 ni = make_float2(-is.x, -is.y), nf = make_float2(-fs.x, -fs.y);
-          auto two = [&](float& a0, float& a1, float2 it, float2 ft, int l, unsigned w) {
-            const float2 d = __fadd2_rn(__fadd2_rn(it, ni), __fadd2_rn(ft, nf));
-            const float2 y = __fmul2_rn(make_float2(a0, a1), __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), be));
-            a0 = static_cast<unsigned>(s - l) <= w ? y.x : 0.0f;
-            a1 = static_cast<unsigned>(s + 1 - l) <= w ? y.y : 0.0f;
-          };
-          two(r[i], r[i + 1], i0, f0, l0, w0);
-          two(r[i + 2], r[i + 3], i1, f1, l1, w1);
-        };
-        float s0 = 1.0f, s1 = 1.0f;
-        if constexpr (HALF) {
-          float m0 = 0.0f, m1 = 0.0f;
+    const int t0 = 16 * qd + lane / 4, t1 = t0 + 8, cc = 2 * (lane % 4);  // this thread's rows, and columns of 8
 #pragma unroll 1
-          for (int q = 0; q <= qd; ++q) {
-            float r[8];
-            tm_ld_16x16(tw + kPtColScore + 16 * q, r);
-            wait_ld();
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              decayed(2 * q + e, r, 4 * e);
-              m0 = fmaxf(m0, fmaxf(fabsf(r[4 * e]), fabsf(r[4 * e + 1])));
-              m1 = fmaxf(m1, fmaxf(fabsf(r[4 * e + 2]), fabsf(r[4 * e + 3])));
-            }
-          }
-#pragma unroll
-          for (int d = 1; d < 4; d <<= 1) {
-            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
-            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
-          }
-          float k0, k1;
-          s0 = row_scale(m0, k0);
-          s1 = row_scale(m1, k1);
-          if (lane % 4 == 0) {
-            float* sp = reinterpret_cast<float*>(sm + L::kScaleP) + 64 * buf;
-            sp[t0] = k0;
-            sp[t1] = k1;
-          }
-        }
-        // columns right of this warp's diagonal block are never written: zero
-        unsigned char* pb = sm + L::kP + buf * L::kPanel + t0 * 128 + 2 * cc;
+    for (; outputs; ++g) {
+      const int st = g % NST, buf = g & 1;
+      if (!(ok = wait_all(B::kGateFull + st, g / NST)) || chunk_of(g).n < 0) break;
+      if (!(ok = wait_all(B::kPFree + buf, (g >> 1) - 1) && wait_all(B::kScFull, g))) break;
+      fence_after();
+      const float* f = gate_of(g);
+      const int* first = reinterpret_cast<const int*>(f + Gate::kFirst);
+      const float2 i0 = f2(f[Gate::kInt + t0]), i1 = f2(f[Gate::kInt + t1]);
+      const float2 f0 = f2(f[Gate::kFrac + t0]), f1 = f2(f[Gate::kFrac + t1]);
+      const int l0 = first[t0], l1 = first[t1];
+      const unsigned w0 = t0 - l0, w1 = t1 - l1;
+      // the decayed scores of columns 8j + cc and the next, in place
+      auto decayed = [&](int j, float (&r)[8], int i) {
+        const int s = 8 * j + cc;
+        auto at = [&](int k) { return *reinterpret_cast<const float2*>(f + k + s); };
+        const float2 is = at(Gate::kInt), fs = at(Gate::kFrac), be = at(Gate::kBeta);
+        const float2 ni = make_float2(-is.x, -is.y), nf = make_float2(-fs.x, -fs.y);
+        auto two = [&](float& a0, float& a1, float2 it, float2 ft, int l, unsigned w) {
+          const float2 d = __fadd2_rn(__fadd2_rn(it, ni), __fadd2_rn(ft, nf));
+          const float2 y = __fmul2_rn(make_float2(a0, a1), __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), be));
+          a0 = static_cast<unsigned>(s - l) <= w ? y.x : 0.0f;
+          a1 = static_cast<unsigned>(s + 1 - l) <= w ? y.y : 0.0f;
+        };
+        two(r[i], r[i + 1], i0, f0, l0, w0);
+        two(r[i + 2], r[i + 3], i1, f1, l1, w1);
+      };
+      float s0 = 1.0f, s1 = 1.0f;
+      if constexpr (HALF) {
+        float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll 1
         for (int q = 0; q <= qd; ++q) {
           float r[8];
@@ -653,115 +648,136 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           wait_ld();
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int j = 2 * q + e;
-            decayed(j, r, 4 * e);
-            const int at = (j ^ (t0 & 7)) << 4;  // t1 & 7 is the same
-            if constexpr (HALF) {
-              r[4 * e] *= s0;
-              r[4 * e + 1] *= s0;
-              r[4 * e + 2] *= s1;
-              r[4 * e + 3] *= s1;
-            }
-            *reinterpret_cast<uint32_t*>(pb + at) = E::narrow2(r[4 * e], r[4 * e + 1]);
-            *reinterpret_cast<uint32_t*>(pb + 1024 + at) = E::narrow2(r[4 * e + 2], r[4 * e + 3]);
+            decayed(2 * q + e, r, 4 * e);
+            m0 = fmaxf(m0, fmaxf(fabsf(r[4 * e]), fabsf(r[4 * e + 1])));
+            m1 = fmaxf(m1, fmaxf(fabsf(r[4 * e + 2]), fabsf(r[4 * e + 3])));
           }
         }
-        fence_before();
-        fence_async_smem();
-        signal(B::kPFull + buf);
-        if (lane == 0) {
-          arrive(bar(B::kScFree));
-          arrive(bar(B::kGateFree + st));
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
         }
-        return true;
-      };
-      for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x)
-        for (int c = item_at(it).chunks; ok && c > 0; --c, ++g) ok = form_p(g);
+        float k0, k1;
+        s0 = row_scale(m0, k0);
+        s1 = row_scale(m1, k1);
+        if (lane % 4 == 0) {
+          float* sp = reinterpret_cast<float*>(sm + L::kScaleP) + 64 * buf;
+          sp[t0] = k0;
+          sp[t1] = k1;
+        }
+      }
+      // columns right of this warp's diagonal block are never written: zero
+      unsigned char* pb = sm + L::kP + buf * L::kPanel + t0 * 128 + 2 * cc;
+#pragma unroll 1
+      for (int q = 0; q <= qd; ++q) {
+        float r[8];
+        tm_ld_16x16(tw + kPtColScore + 16 * q, r);
+        wait_ld();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = 2 * q + e;
+          decayed(j, r, 4 * e);
+          const int at = (j ^ (t0 & 7)) << 4;  // t1 & 7 is the same
+          if constexpr (HALF) {
+            r[4 * e] *= s0;
+            r[4 * e + 1] *= s0;
+            r[4 * e + 2] *= s1;
+            r[4 * e + 3] *= s1;
+          }
+          *reinterpret_cast<uint32_t*>(pb + at) = E::narrow2(r[4 * e], r[4 * e + 1]);
+          *reinterpret_cast<uint32_t*>(pb + 1024 + at) = E::narrow2(r[4 * e + 2], r[4 * e + 3]);
+        }
+      }
+      fence_before();
+      fence_async_smem();
+      signal(B::kPFull + buf);
+      if (lane == 0) {
+        arrive(bar(B::kScFree));
+        arrive(bar(B::kGateFree + st));
+      }
     }
   } else if (warp < 12) {
     // ---- outputs
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (outputs) {
-      constexpr int WR = MDV / 4;  // rows of a warp
-      const int m = lane >> 3;     // the matrix whose row address this lane gives to stmatrix
-      for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-        const Item x = item_at(it);
-        const int row = x.blk * MDV + WR * qd;  // the warp's first row
-        for (int c = 0; c < x.chunks; ++c, ++g) {
-          if (!(ok = wait_all(B::kOFull, g))) break;
-          fence_after();
-          const int st = g % NST;
-          const float* eg = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot) + Gate::kDecay + 2 * (lane % 4);
-          const float* sp = reinterpret_cast<const float*>(sm + L::kScaleP) + 64 * (g & 1) + 2 * (lane % 4);
-          const float* ss = reinterpret_cast<const float*>(sm + L::kScaleS) + 128 * (g & 1) + WR * qd + lane / 4;
-          const int t = x.begin + c * C, n = x.end - t;
-          // the contractions are done with q and k: their place holds this
-          // warp's outputs [64 tokens][WR rows], swizzled as the store wants
-          const uint32_t out = base + st * L::kStage + qd * (C * WR * 2);
+    constexpr int WR = MDV / 4;  // rows of a warp
+    const int m = lane >> 3;     // the matrix whose row address this lane gives to stmatrix
 #pragma unroll 1
-          for (int i = 0; i < WR / 16 * 4; ++i) {
-            const int h = i >> 2, q = i & 3;  // 16 rows, 16 tokens
-            const uint32_t from = tw + (static_cast<uint32_t>(16 * h) << 16) + 16 * q;
-            float u[8], y[8];
-            tm_ld_16x16(from + kPtColO1, u);
-            tm_ld_16x16(from + kPtColO2, y);
-            const float sa = HALF ? ss[16 * h] : 1.0f, sb = HALF ? ss[16 * h + 8] : 1.0f;
-            wait_ld();
-            uint32_t w[4];
+    for (; outputs; ++g) {
+      const int st = g % NST;
+      if (!(ok = wait_all(B::kGateFull + st, g / NST)) || chunk_of(g).n < 0) break;
+      const int t = chunk_of(g).t, n = chunk_of(g).n, head = chunk_of(g).head;
+      const int row = chunk_of(g).row + WR * qd;  // the warp's first row
+      if (!(ok = wait_all(B::kOFull, g))) break;
+      fence_after();
+      const float* eg = gate_of(g) + Gate::kDecay + 2 * (lane % 4);
+      const float* sp = reinterpret_cast<const float*>(sm + L::kScaleP) + 64 * (g & 1) + 2 * (lane % 4);
+      const float* ss = reinterpret_cast<const float*>(sm + L::kScaleS) + 128 * (g & 1) + WR * qd + lane / 4;
+      // the contractions are done with q and k: their place holds this
+      // warp's outputs [64 tokens][WR rows], swizzled as the store wants
+      const uint32_t out = base + st * L::kStage + qd * (C * WR * 2);
+#pragma unroll 1
+      for (int i = 0; i < WR / 16 * 4; ++i) {
+        const int h = i >> 2, q = i & 3;  // 16 rows, 16 tokens
+        const uint32_t from = tw + (static_cast<uint32_t>(16 * h) << 16) + 16 * q;
+        float u[8], y[8];
+        tm_ld_16x16(from + kPtColO1, u);
+        tm_ld_16x16(from + kPtColO2, y);
+        const float sa = HALF ? ss[16 * h] : 1.0f, sb = HALF ? ss[16 * h + 8] : 1.0f;
+        wait_ld();
+        uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 d = *reinterpret_cast<const float2*>(eg + 16 * q + 8 * e);
-              float2 ya = make_float2(y[4 * e], y[4 * e + 1]), yb = make_float2(y[4 * e + 2], y[4 * e + 3]);
-              float2 da = d, db = d;
-              if constexpr (HALF) {
-                const float2 k = *reinterpret_cast<const float2*>(sp + 16 * q + 8 * e);
-                ya = __fmul2_rn(k, ya);
-                yb = __fmul2_rn(k, yb);
-                da = __fmul2_rn(d, f2(sa));
-                db = __fmul2_rn(d, f2(sb));
-              }
-              const float2 oa = __ffma2_rn(da, make_float2(u[4 * e], u[4 * e + 1]), ya);
-              const float2 ob = __ffma2_rn(db, make_float2(u[4 * e + 2], u[4 * e + 3]), yb);
-              w[2 * e] = E::narrow2(oa.x, oa.y);
-              w[2 * e + 1] = E::narrow2(ob.x, ob.y);
-            }
-            // matrices: rows 16h.. and 16h + 8.. of two blocks of 8 tokens
-            const int tt = 16 * q + 8 * (m >> 1) + (lane & 7), chunk = 2 * h + (m & 1);
-            const int sw = WR == 32 ? (tt >> 1) & 3 : (tt >> 2) & 1;
-            stsm4_t(out + tt * (2 * WR) + ((chunk ^ sw) << 4), w[0], w[1], w[2], w[3]);
+        for (int e = 0; e < 2; ++e) {
+          const float2 d = *reinterpret_cast<const float2*>(eg + 16 * q + 8 * e);
+          float2 ya = make_float2(y[4 * e], y[4 * e + 1]), yb = make_float2(y[4 * e + 2], y[4 * e + 3]);
+          float2 da = d, db = d;
+          if constexpr (HALF) {
+            const float2 k = *reinterpret_cast<const float2*>(sp + 16 * q + 8 * e);
+            ya = __fmul2_rn(k, ya);
+            yb = __fmul2_rn(k, yb);
+            da = __fmul2_rn(d, f2(sa));
+            db = __fmul2_rn(d, f2(sb));
           }
-          fence_before();
-          fence_async_smem();
-          signal(B::kOFree);
-          if (lane == 0) arrive(bar(B::kGateFree + st));
-          if (n >= C) {
-            if (lane == 0 && row < p.dv) tma_store3(&mo, out, row, x.head, t);
-          } else {
-            // a prompt's end: only its own rows
-            constexpr int PER = WR / 8;  // 16-byte pieces of a token
-            const int piece = lane % PER;
-            if (row + 8 * piece < p.dv) {
-              T* o = static_cast<T*>(p.o) + static_cast<size_t>(t) * p.o_stride + static_cast<size_t>(x.head) * p.dv + row +
-                     8 * piece;
+          const float2 oa = __ffma2_rn(da, make_float2(u[4 * e], u[4 * e + 1]), ya);
+          const float2 ob = __ffma2_rn(db, make_float2(u[4 * e + 2], u[4 * e + 3]), yb);
+          w[2 * e] = E::narrow2(oa.x, oa.y);
+          w[2 * e + 1] = E::narrow2(ob.x, ob.y);
+        }
+        // matrices: rows 16h.. and 16h + 8.. of two blocks of 8 tokens
+        const int tt = 16 * q + 8 * (m >> 1) + (lane & 7), chunk = 2 * h + (m & 1);
+        const int sw = WR == 32 ? (tt >> 1) & 3 : (tt >> 2) & 1;
+        stsm4_t(out + tt * (2 * WR) + ((chunk ^ sw) << 4), w[0], w[1], w[2], w[3]);
+      }
+      fence_before();
+      fence_async_smem();
+      signal(B::kOFree);
+      if (lane == 0) arrive(bar(B::kGateFree + st));
+      if (n == C) {
+        if (lane == 0 && row < p.dv) tma_store3(&mo, out, row, head, t);
+      } else {
+        // a prompt's end: only its own rows
+        constexpr int PER = WR / 8;  // 16-byte pieces of a token
+        const int piece = lane % PER;
+        if (row + 8 * piece < p.dv) {
+          T* o = static_cast<T*>(p.o) + static_cast<size_t>(t) * p.o_stride + static_cast<size_t>(head) * p.dv + row +
+                 8 * piece;
 #pragma unroll 1
-              for (int tt = lane / PER; tt < n; tt += 32 / PER) {
-                const int sw = WR == 32 ? (tt >> 1) & 3 : (tt >> 2) & 1;
-                *reinterpret_cast<uint4*>(o + tt * p.o_stride) = *reinterpret_cast<const uint4*>(
-                    sm + (out - base) + tt * (2 * WR) + ((piece ^ sw) << 4));
-              }
-            }
+          for (int tt = lane / PER; tt < n; tt += 32 / PER) {
+            const int sw = WR == 32 ? (tt >> 1) & 3 : (tt >> 2) & 1;
+            *reinterpret_cast<uint4*>(o + tt * p.o_stride) =
+                *reinterpret_cast<const uint4*>(sm + (out - base) + tt * (2 * WR) + ((piece ^ sw) << 4));
           }
-          // the stage before this one is free once its store has read it
-          if (lane == 0) {
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-          }
-          if (g > 0) signal(B::kEmpty + (g - 1) % NST);
         }
       }
+      // the stage before this one is free once its store has read it
+      if (lane == 0) {
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      }
+      if (g > 0) signal(B::kEmpty + (g - 1) % NST);
     }
   } else {
-    // ---- W(g + 1), then the state behind chunk g
+    // ---- the state into tensor memory, W one chunk ahead, the state's update
     asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     const int half = (warp - 12) >> 2;  // which half of W's tokens and of S's columns
     constexpr int SC = DK / 2;
@@ -776,13 +792,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     auto worst = [&](int buf, int row) { return fmaxf(maxima[256 * buf + row], maxima[256 * buf + 128 + row]); };
     // A thread holds rows T/4 and T/4 + 8 of each 16, tokens 8j + 2 (T%4)
     // and the next of the warpgroup's 32.
-    auto form_w = [&](int n, int count) -> bool {  // `count`: tokens left in the prompt
+    auto form_w = [&](int n) -> bool {
       const int st = n % NST;
-      if (!wait_all(B::kFull + st, n / NST) || !wait_all(B::kGateFull + st, n / NST)) return false;
+      const int count = chunk_of(n).n;
+      if (!wait_all(B::kFull + st, n / NST)) return false;
       const uint32_t s = base + st * L::kStage;
       if (count < C) {
         // the rows behind the prompt's end belong to others: zeros for the contractions
         const int n16 = (C - count) * 8;
+#pragma unroll 1
         for (int i = tid - 384; i < n16 * ((DK + MDV) / 64); i += 256) {
           const int panel = i / n16, j = i % n16;
           *reinterpret_cast<uint4*>(sm + st * L::kStage + L::kK + panel * L::kPanel + (count + j / 8) * 128 +
@@ -790,7 +808,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         fence_async_smem();
       }
-      const float* wt = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot) + Gate::kW + 32 * half + 2 * (lane % 4);
+      const float* wt = gate_of(n) + Gate::kW + 32 * half + 2 * (lane % 4);
       const int m = lane >> 3;  // the matrix whose row address this lane gives to ldmatrix
       // w v of rows 16h.. and tokens 16q..: pairs of tokens 8j + 2 (T%4) and
       // the next, [j][0] of row T/4, [j][1] of row T/4 + 8
@@ -815,7 +833,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll 1
         for (int h = 0; h < MDV / 64; ++h) {
           float m0 = 0.0f, m1 = 0.0f;
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < 2; ++q) {
             float2 x[2][2];
             values(h, q, x);
@@ -872,21 +890,21 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       if (lane == 0) arrive(bar(B::kEmpty + st));
       return true;
     };
-    // the state before chunk n into tensor memory, rounded to E
-    auto put_state = [&](int n) -> bool {
+    // the state before chunk g into tensor memory, rounded to E
+    auto put_state = [&]() -> bool {
       float up = 1.0f;
       if constexpr (HALF) {
         float m = 0.0f, back;
 #pragma unroll
         for (int j = 0; j < SC / 2; ++j) m = fmaxf(m, fmaxf(fabsf(S[j].x), fabsf(S[j].y)));
-        const int buf = 4 + (n & 1);
+        const int buf = 4 + (g & 1);
         if (irow >= 0) maxima[256 * buf + 128 * half + irow] = m;
         if (!pair()) return false;
         up = row_scale(worst(buf, max(irow, 0)), back);
-        if (!wait_all(B::kO1Done, n - 1)) return false;
-        if (half == 0 && irow >= 0) reinterpret_cast<float*>(sm + L::kScaleS)[128 * (n & 1) + irow] = back;
+        if (!wait_all(B::kO1Done, g - 1)) return false;
+        if (half == 0 && irow >= 0) reinterpret_cast<float*>(sm + L::kScaleS)[128 * (g & 1) + irow] = back;
       } else {
-        if (!wait_all(B::kO1Done, n - 1)) return false;
+        if (!wait_all(B::kO1Done, g - 1)) return false;
       }
       fence_after();
 #pragma unroll
@@ -905,17 +923,21 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       return true;
     };
     // this thread's part of a head's state, or null where it has none
-    auto part = [&](const float* state, int blk) {
-      const int row = blk * MDV + irow;
+    auto part = [&](const float* state, int row) {
+      row += irow;
       return irow >= 0 && row < p.dv && state != nullptr ? const_cast<float*>(state) + static_cast<size_t>(row) * DK + SC * half
                                                          : nullptr;
     };
-    for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-      int tokens;
-      {
-        const Item x = item_at(it);
-        tokens = x.end - x.begin;
-        const float* from = part(x.from, x.blk);
+    float decay = 1.0f;  // of the item so far
+    bool more = (ok = wait_all(B::kGateFull, 0)) && chunk_of(0).n >= 0;
+    if (more) ok = form_w(0);
+#pragma unroll 1
+    for (; ok && more; ++g) {
+      if (chunk_of(g).first) {
+        decay = 1.0f;
+        const float* from = part(chunk_of(g).from, chunk_of(g).row);
+#pragma unroll
+        for (int j = 0; j < SC / 2; ++j) S[j] = f2(0.0f);
         if (from != nullptr) {
 #pragma unroll
           for (int j = 0; j < SC; j += 8) {
@@ -924,61 +946,51 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[j / 2 + i] = make_float2(v[2 * i], v[2 * i + 1]);
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < SC / 2; ++j) S[j] = f2(0.0f);
         }
       }
-      float decay = 1.0f;  // of the item so far
-      if (tokens > 0) {
-        if (g == 0) ok = form_w(0, tokens);
-        if (ok && outputs) ok = put_state(g);
-      }
-      for (; ok && tokens > 0; tokens -= C, ++g) {
-        const int count = tokens > C ? tokens - C : count_behind(it);
-        if (count > 0) ok = form_w(g + 1, count);
-        if (!ok || !(ok = wait_all(B::kKvFull, g))) break;
-        fence_after();
-        const int st = g % NST;
-        const float gamma = reinterpret_cast<const float*>(sm + L::kGate + st * L::kGateSlot)[Gate::kLast];
-        float back = 1.0f;
-        if constexpr (HALF) row_scale(worst(g & 3, max(irow, 0)), back);
-        decay *= gamma;
+      if (outputs && !(ok = put_state())) break;
+      if (!(ok = wait_all(B::kGateFull + (g + 1) % NST, (g + 1) / NST))) break;
+      more = chunk_of(g + 1).n >= 0;
+      if (more && !(ok = form_w(g + 1))) break;
+      if (!(ok = wait_all(B::kKvFull, g))) break;
+      fence_after();
+      const float gamma = chunk_of(g).last;
+      decay *= gamma;
+      float back = 1.0f;
+      if constexpr (HALF) row_scale(worst(g & 3, max(irow, 0)), back);
 #pragma unroll
-        for (int q = 0; q < SC / 16; ++q) {
-          float r[16];
-          tm_ld16(tw + kPtColKV + SC * half + 16 * q, r);
-          wait_ld();
-          if (q == SC / 16 - 1) {
-            fence_before();
-            signal(B::kKvFree);
-            if (lane == 0) arrive(bar(B::kGateFree + st));
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float2 v = make_float2(r[2 * e], r[2 * e + 1]);
-            if constexpr (HALF) v = __fmul2_rn(v, f2(back));
-            S[8 * q + e] = __ffma2_rn(S[8 * q + e], f2(gamma), v);
-          }
+      for (int q = 0; q < SC / 16; ++q) {
+        float r[16];
+        tm_ld16(tw + kPtColKV + SC * half + 16 * q, r);
+        wait_ld();
+        if (q == SC / 16 - 1) {
+          fence_before();
+          signal(B::kKvFree);
         }
-        if (outputs && tokens > C) ok = put_state(g + 1);
-      }
-      if (!ok) break;
-      const Item x = item_at(it);
-      float* to = part(x.to, x.blk);
-      if (to != nullptr) {
 #pragma unroll
-        for (int j = 0; j < SC; j += 8) {
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[2 * i] = S[j / 2 + i].x;
-            v[2 * i + 1] = S[j / 2 + i].y;
-          }
-          store8<F32>(to + j, v);
+        for (int e = 0; e < 8; ++e) {
+          float2 v = make_float2(r[2 * e], r[2 * e + 1]);
+          if constexpr (HALF) v = __fmul2_rn(v, f2(back));
+          S[8 * q + e] = __ffma2_rn(S[8 * q + e], f2(gamma), v);
         }
       }
-      if (x.decay != nullptr && tid == 384 && x.blk == 0) *x.decay = decay;
+      if (chunk_of(g).final) {
+        float* to = part(chunk_of(g).to, chunk_of(g).row);
+        if (to != nullptr) {
+#pragma unroll
+          for (int j = 0; j < SC; j += 8) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[2 * i] = S[j / 2 + i].x;
+              v[2 * i + 1] = S[j / 2 + i].y;
+            }
+            store8<F32>(to + j, v);
+          }
+        }
+        if (chunk_of(g).decay != nullptr && tid == 384 && chunk_of(g).row == 0) *chunk_of(g).decay = decay;
+      }
+      signal(B::kGateFree + g % NST);
     }
   }
 
