@@ -7,9 +7,9 @@
 //   o_t    = 2^{G_t} S q_t + sum_{s<=t} (q_t . k_s) 2^{G_t - G_s} beta_s v_s
 //   S_out  = 2^{G_C} S + sum_s (2^{G_C - G_s} beta_s v_s) k_s^T
 // Only differences G_t - G_s with s <= t are exponentiated, so nothing
-// overflows.  G is summed in FP64 and kept as an integer and a fraction, each
-// exact enough in FP32 that a difference of neighbours far down a chunk is off
-// by 2^-23, whatever the decays before them.  A decay below 2^-120 is a
+// overflows.  G is summed in fixed point and kept as an integer and a
+// fraction, each exact enough in FP32 that a difference of neighbours far down
+// a chunk is off by 2^-23, whatever the decays before them.  A decay below 2^-120 is a
 // reset: it leaves the running sum alone and cuts the tokens before it off.
 //
 // One CTA per SM works on (prompt, head, block of MDV rows of S) items, one
@@ -34,8 +34,8 @@
 // their rows, taken out again in FP32.
 //
 // Warps: 0 loads q, k, v by TMA (128-byte swizzle, a ring of stages); 1
-// issues the contractions; 2 turns alpha and beta into the chunk's factors; 3
-// holds the tensor memory; 4-7 form P from the scores; 8-11 write the
+// issues O1 and O2, 3 the scores and KV; 2 says what each chunk is and turns
+// alpha and beta into its factors; 4-7 form P from the scores; 8-11 write the
 // outputs; 12-19 form W and own the state (each of the two warpgroups half of
 // W's tokens and half of S's columns).  All hand-offs are mbarriers; every
 // wait is bounded, and on a timeout the CTA counts it, waits for its copies,
@@ -96,9 +96,10 @@ struct PtLayout {
   static constexpr int kGate = kP + 2 * kPanel;         // per stage, see Gate
   static constexpr int kGateSlot = 6 * 256 + 128;
   static constexpr int kScaleS = kGate + kStages * kGateSlot;  // fp16: 2 x 128 row scales of S
-  static constexpr int kScaleP = kScaleS + 1024;               // fp16: 2 x 64 row scales of P
-  static constexpr int kMax = kScaleP + 512;                   // fp16: 6 x 2 x 128 row maxima, 4 of W and 2 of S
-  static constexpr int kBars = kMax + 6144;
+  static constexpr int kScaleP = kScaleS + 1024;               // fp16: 4 x 64 row scales of P
+  static constexpr int kMax = kScaleP + 1024;                  // fp16: 6 x 2 x 128 row maxima, 4 of W and 2 of S
+  static constexpr int kSeen = kMax + 6144;                    // chunks whose gates are being loaded
+  static constexpr int kBars = kSeen + 256;
   static constexpr int kBytes = kBars + 320 + 1024;
 };
 
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) {
       bar_init(bar(B::kFull + s), 1);
-      bar_init(bar(B::kEmpty + s), outputs ? 4 + 8 : 1 + 8);  // the outputs' warps, or the contractions; W's warps
+      bar_init(bar(B::kEmpty + s), outputs ? 4 + 8 : 8);       // the outputs' warps, the state's warps
       bar_init(bar(B::kGateFull + s), 1);
       bar_init(bar(B::kGateFree + s), outputs ? 4 + 4 + 8 : 8);  // its readers
     }
@@ -448,55 +449,45 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           for (int j = max(0, g - NST); j < g; ++j) mbar_wait(bar(B::kFull + j % NST), (j / NST) & 1, 1 << 16);
       }
     } else if (warp == 1) {
-      // ---- contractions: KV(g), O1(g), scores(g + 1), O2(g).  The whole warp
-      // runs the loop, so that addresses stay uniform; one lane issues.
-      constexpr uint32_t id_sc = idesc<E>(C, C, false, false), id_kv = idesc<E>(MDV, DK, false, true),
-                         id_o1 = idesc<E>(MDV, C, false, false), id_o2 = idesc<E>(MDV, C, true, false);
+      // ---- contractions: the outputs' two.  The whole warp runs the loop, so
+      // that addresses stay uniform; one lane issues.
+      constexpr uint32_t id_o1 = idesc<E>(MDV, C, false, false), id_o2 = idesc<E>(MDV, C, true, false);
       // descriptors of stage 0; a byte offset adds a sixteenth of itself
-      const uint64_t dq = desc128(base + L::kQ, 16), dk = desc128(base + L::kK, 16),
-                     dkt = desc128(base + L::kK, L::kPanel), dv = desc128(base + L::kV, L::kPanel),
-                     dp = desc128(base + L::kP, 16);
-      // The gate slot of chunk n is full: is there one?
-      auto exists = [&](int n) -> bool {
-        if (!(ok = wait_all(B::kGateFull + n % NST, n / NST))) return false;
-        return chunk_of(n).n >= 0;
-      };
-      bool more = exists(0);
-      // scores(0) starts the pipeline; from then on, scores(g + 1) follow O1(g)
-      int n = outputs ? 0 : 1;
+      const uint64_t dq = desc128(base + L::kQ, 16), dv = desc128(base + L::kV, L::kPanel), dp = desc128(base + L::kP, 16);
 #pragma unroll 1
-      while (ok && more) {
-        if (n > g) {  // chunk g's own contractions
-          const uint32_t s = (g % NST) * (L::kStage / 16);
-          // W's warps have waited for this stage's loads; so have the scores
-          if (!(ok = wait_all(B::kWFull + (g & 1), g >> 1) && wait_all(B::kKvFree, g - 1))) break;
-          if (!outputs && !(ok = wait_all(B::kFull + g % NST, g / NST))) break;
-          fence_after();
-          if (elect_one()) {
-            const uint32_t w = tm + kPtColW + 64 * (g & 1);
+      for (; outputs; ++g) {
+        const uint32_t s = (g % NST) * (L::kStage / 16), pb = (g & 1) * (L::kPanel / 16);
+        if (!(ok = wait_all(B::kGateFull + g % NST, g / NST)) || chunk_of(g).n < 0) break;
+        // the state's warps have waited for this stage's loads
+        if (!(ok = wait_all(B::kSFull, g) && wait_all(B::kOFree, g - 1))) break;
+        fence_after();
+        if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < C / 8; ++k)  // 4 steps of W's value, 4 of its rounding error
-              mma16_ts(tm + kPtColKV, w + 8 * k, dkt + (s + (k % 4) * (2048 / 16)), id_kv, k > 0);
-            mma_commit(bar(B::kKvFull));
-            if (!outputs) mma_commit(bar(B::kEmpty + g % NST));
-          }
-          __syncwarp();
-          more = exists(g + 1);
-          if (!ok) break;
-          if (outputs) {
-            if (!(ok = wait_all(B::kSFull, g) && wait_all(B::kOFree, g - 1))) break;
-            fence_after();
-            if (elect_one()) {
-#pragma unroll
-              for (int k = 0; k < DK / 16; ++k)
-                mma16_ts(tm + kPtColO1, tm + kPtColS + 8 * k, dq + (s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16), id_o1,
-                         k > 0);
-              mma_commit(bar(B::kO1Done));
-            }
-            __syncwarp();
-          }
+          for (int k = 0; k < DK / 16; ++k)
+            mma16_ts(tm + kPtColO1, tm + kPtColS + 8 * k, dq + (s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16), id_o1, k > 0);
+          mma_commit(bar(B::kO1Done));
         }
-        if (outputs && more) {  // scores(n)
+        __syncwarp();
+        if (!(ok = wait_all(B::kPFull + (g & 1), g >> 1))) break;
+        fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < C / 16; ++k)
+            mma16_ss(tm + kPtColO2, dv + (s + k * (2048 / 16)), dp + (pb + 2 * k), id_o2, k > 0);
+          mma_commit(bar(B::kOFull));
+          mma_commit(bar(B::kPFree + (g & 1)));
+        }
+        __syncwarp();
+      }
+    } else if (warp == 3) {
+      // ---- contractions: scores(g + 1) and KV(g)
+      constexpr uint32_t id_sc = idesc<E>(C, C, false, false), id_kv = idesc<E>(MDV, DK, false, true);
+      const uint64_t dq = desc128(base + L::kQ, 16), dk = desc128(base + L::kK, 16), dkt = desc128(base + L::kK, L::kPanel);
+#pragma unroll 1
+      for (int n = 0;; ++n) {
+        if (!(ok = wait_all(B::kGateFull + n % NST, n / NST))) break;
+        const bool more = chunk_of(n).n >= 0;
+        if (outputs && more) {
           if (!(ok = wait_all(B::kFull + n % NST, n / NST) && wait_all(B::kScFree, n - 1))) break;
           fence_after();
           if (elect_one()) {
@@ -510,74 +501,87 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           }
           __syncwarp();
         }
-        if (n > g) {
-          if (outputs) {
-            const uint32_t s = (g % NST) * (L::kStage / 16), pb = (g & 1) * (L::kPanel / 16);
-            if (!(ok = wait_all(B::kPFull + (g & 1), g >> 1))) break;
-            fence_after();
-            if (elect_one()) {
+        if (n > 0) {
+          g = n - 1;
+          if (!(ok = wait_all(B::kWFull + (g & 1), g >> 1) && wait_all(B::kKvFree, g - 1))) break;
+          fence_after();
+          if (elect_one()) {
+            const uint32_t s = (g % NST) * (L::kStage / 16), w = tm + kPtColW + 64 * (g & 1);
 #pragma unroll
-              for (int k = 0; k < C / 16; ++k)
-                mma16_ss(tm + kPtColO2, dv + (s + k * (2048 / 16)), dp + (pb + 2 * k), id_o2, k > 0);
-              mma_commit(bar(B::kOFull));
-              mma_commit(bar(B::kPFree + (g & 1)));
-            }
-            __syncwarp();
+            for (int k = 0; k < C / 8; ++k)  // 4 steps of W's value, 4 of its rounding error
+              mma16_ts(tm + kPtColKV, w + 8 * k, dkt + (s + (k % 4) * (2048 / 16)), id_kv, k > 0);
+            mma_commit(bar(B::kKvFull));
           }
-          ++g;
+          __syncwarp();
         }
-        ++n;
+        if (!more) break;
       }
     } else if (warp == 2) {
       // ---- what each chunk is, and its factors from alpha and beta, whose
-      // loads are issued a chunk ahead
-      struct Ahead {
-        float a0, a1, b0, b1;
-        Chunk c;
+      // loads are issued kAhead chunks ahead (a token's gates of one head are
+      // alone in their sector, so they take a full trip to memory)
+      constexpr int kAhead = 2;
+      struct Gates {
+        float a0 = 1.0f, a1 = 1.0f, b0 = 0.0f, b1 = 0.0f;
       };
-      int it = blockIdx.x, c = 0;
+      Chunk* const seen = reinterpret_cast<Chunk*>(sm + L::kSeen);  // the chunks whose loads are in flight
+      int it = blockIdx.x, c = 0, loaded = 0;
       Item x{};
-      auto load = [&](Ahead& r) {  // the next chunk; n < 0: none
+      auto load = [&]() -> Gates {  // the next chunk's
+        Gates r;
+        Chunk k;
+        k.n = -1;
         if (c == x.chunks) {
           c = 0;
+#pragma unroll 1
           for (x.chunks = 0; it < a.items && x.chunks == 0; it += gridDim.x) x = item_at(it);
         }
-        r.a0 = r.a1 = 1.0f;
-        r.b0 = r.b1 = 0.0f;
-        r.c.n = -1;
-        if (x.chunks == 0) return;
-        r.c.t = x.begin + c * C;
-        r.c.n = min(x.end - r.c.t, C);
-        r.c.head = x.head;
-        r.c.row = x.blk * MDV;
-        r.c.first = c == 0;
-        r.c.final = ++c == x.chunks;
-        r.c.from = x.from;
-        r.c.to = x.to;
-        r.c.decay = x.decay;
-        const size_t at = static_cast<size_t>(r.c.t + lane) * p.heads + x.head, at1 = at + static_cast<size_t>(32) * p.heads;
-        if (lane < r.c.n) r.a0 = __ldg(p.alpha + at), r.b0 = __ldg(p.beta + at);
-        if (lane + 32 < r.c.n) r.a1 = __ldg(p.alpha + at1), r.b1 = __ldg(p.beta + at1);
+        if (x.chunks > 0) {
+          k.t = x.begin + c * C;
+          k.n = min(x.end - k.t, C);
+          const size_t at = static_cast<size_t>(k.t + lane) * p.heads + x.head;
+          const size_t at1 = at + static_cast<size_t>(32) * p.heads;
+          if (lane < k.n) r.a0 = __ldg(p.alpha + at), r.b0 = __ldg(p.beta + at);
+          if (lane + 32 < k.n) r.a1 = __ldg(p.alpha + at1), r.b1 = __ldg(p.beta + at1);
+          k.head = x.head;
+          k.row = x.blk * MDV;
+          k.first = c == 0;
+          k.final = ++c == x.chunks;
+          k.from = x.from;
+          k.to = x.to;
+          k.decay = x.decay;
+        }
+        if (lane == 0) seen[loaded % (kAhead + 1)] = k;
+        ++loaded;
+        return r;
       };
-      Ahead next;
-      load(next);
+      Gates ahead[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) ahead[i] = load();
 #pragma unroll 1
-      for (bool more = true; more; ++g) {
-        const Ahead now = next;
-        more = now.c.n >= 0;
-        if (more) load(next);
+      for (;; ++g) {
+        const Gates now = ahead[0];
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+        ahead[kAhead - 1] = load();
         const bool z0 = now.a0 < kPtReset, z1 = now.a1 < kPtReset;
-        double x0 = z0 ? 0.0 : static_cast<double>(log2f(now.a0)), x1 = z1 ? 0.0 : static_cast<double>(log2f(now.a1));
-#pragma unroll 1
+        // the running sum of log2(alpha), in units of 2^-32
+        auto fixed = [](float v) { return __float2ll_rn(v * 0x1p32f); };
+        auto real = [](long long v) { return __ll2float_rn(v) * 0x1p-32f; };
+        long long x0 = z0 ? 0 : fixed(log2f(now.a0)), x1 = z1 ? 0 : fixed(log2f(now.a1));
+#pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-          const double y0 = __shfl_up_sync(0xffffffffu, x0, d), y1 = __shfl_up_sync(0xffffffffu, x1, d);
+          const long long y0 = __shfl_up_sync(0xffffffffu, x0, d), y1 = __shfl_up_sync(0xffffffffu, x1, d);
           if (lane >= d) {
             x0 += y0;
             x1 += y1;
           }
         }
         x1 += __shfl_sync(0xffffffffu, x0, 31);
-        const double gc = __shfl_sync(0xffffffffu, x1, 31);
+        const long long gc = __shfl_sync(0xffffffffu, x1, 31);
+        // NaN and infinite decays (which the fixed point cannot hold) spoil
+        // their prompt from here on, as they should
+        const float bad = __any_sync(0xffffffffu, !(now.a0 < INFINITY && now.a1 < INFINITY)) ? NAN : 0.0f;
         // the last reset at or before a token: what lies before it is forgotten
         const uint32_t m0 = __ballot_sync(0xffffffffu, z0), m1 = __ballot_sync(0xffffffffu, z1);
         const uint32_t le = 0xffffffffu >> (31 - lane);
@@ -588,23 +592,25 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (!(ok = wait_all(B::kGateFree + g % NST, g / NST - 1))) break;
         float* f = gate_of(g);
         int* first = reinterpret_cast<int*>(f + Gate::kFirst);
-        auto put = [&](int t, double x, float be, int r) {
-          const double whole = rint(x);
-          f[Gate::kInt + t] = static_cast<float>(whole);
-          f[Gate::kFrac + t] = static_cast<float>(x - whole);
+        auto put = [&](int t, long long x, float be, int r) {
+          f[Gate::kInt + t] = static_cast<float>(static_cast<int>(x >> 32));
+          f[Gate::kFrac + t] = __uint2float_rn(static_cast<uint32_t>(x)) * 0x1p-32f + bad;
           f[Gate::kBeta + t] = be;
-          f[Gate::kW + t] = t >= rc ? be * ex2(static_cast<float>(gc - x)) : 0.0f;
-          f[Gate::kDecay + t] = r < 0 ? exp2f(static_cast<float>(x)) : 0.0f;
+          f[Gate::kW + t] = t >= rc ? be * ex2(real(gc - x)) : 0.0f;
+          f[Gate::kDecay + t] = r < 0 ? exp2f(real(x)) : 0.0f;
           first[t] = max(r, 0);
         };
         put(lane, x0, now.b0, r0);
         put(lane + 32, x1, now.b1, r1);
+        __syncwarp();
+        const int n = seen[g % (kAhead + 1)].n;
         if (lane == 0) {
-          Chunk k = now.c;
-          k.last = rc < 0 ? exp2f(static_cast<float>(gc)) : 0.0f;
+          Chunk k = seen[g % (kAhead + 1)];
+          k.last = (rc < 0 ? exp2f(real(gc)) : 0.0f) + bad;
           *reinterpret_cast<Chunk*>(f + Gate::kChunk) = k;
         }
         signal(B::kGateFull + g % NST);
+        if (n < 0) break;
       }
     }
   } else if (warp < 8) {
@@ -662,7 +668,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         s0 = row_scale(m0, k0);
         s1 = row_scale(m1, k1);
         if (lane % 4 == 0) {
-          float* sp = reinterpret_cast<float*>(sm + L::kScaleP) + 64 * buf;
+          float* sp = reinterpret_cast<float*>(sm + L::kScaleP) + 64 * (g & 3);
           sp[t0] = k0;
           sp[t1] = k1;
         }
@@ -711,11 +717,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       if (!(ok = wait_all(B::kOFull, g))) break;
       fence_after();
       const float* eg = gate_of(g) + Gate::kDecay + 2 * (lane % 4);
-      const float* sp = reinterpret_cast<const float*>(sm + L::kScaleP) + 64 * (g & 1) + 2 * (lane % 4);
+      const float* sp = reinterpret_cast<const float*>(sm + L::kScaleP) + 64 * (g & 3) + 2 * (lane % 4);
       const float* ss = reinterpret_cast<const float*>(sm + L::kScaleS) + 128 * (g & 1) + WR * qd + lane / 4;
-      // the contractions are done with q and k: their place holds this
-      // warp's outputs [64 tokens][WR rows], swizzled as the store wants
-      const uint32_t out = base + st * L::kStage + qd * (C * WR * 2);
+      // W is formed and O2 is done with v: its place holds this warp's
+      // outputs [64 tokens][WR rows], swizzled as the store wants
+      const uint32_t out = base + st * L::kStage + L::kV + qd * (C * WR * 2);
 #pragma unroll 1
       for (int i = 0; i < WR / 16 * 4; ++i) {
         const int h = i >> 2, q = i & 3;  // 16 rows, 16 tokens
@@ -857,7 +863,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (!pair()) return false;
       }
       const uint32_t at = tw + kPtColW + 64 * (n & 1) + 16 * half;
-#pragma unroll 1
+#pragma unroll 2
       for (int i = 0; i < MDV / 64 * 2; ++i) {
         const int h = i >> 1, q = i & 1;
         float2 x[2][2];
@@ -887,7 +893,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       wait_st();
       fence_before();
       signal(B::kWFull + (n & 1));
-      if (lane == 0) arrive(bar(B::kEmpty + st));
       return true;
     };
     // the state before chunk g into tensor memory, rounded to E
@@ -991,6 +996,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (chunk_of(g).decay != nullptr && tid == 384 && chunk_of(g).row == 0) *chunk_of(g).decay = decay;
       }
       signal(B::kGateFree + g % NST);
+      if (lane == 0) arrive(bar(B::kEmpty + g % NST));
     }
   }
 
