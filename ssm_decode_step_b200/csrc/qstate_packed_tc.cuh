@@ -216,12 +216,20 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
-// 16 lanes x 16 columns over all 32 threads: registers 4j .. 4j+3 are row
-// T/4 (two columns 8j + 2 (T%4)) and row T/4 + 8 (the same columns).
+// 16 lanes x 16 or 32 columns over all 32 threads: registers 4j .. 4j+3 are
+// row T/4 (two columns 8j + 2 (T%4)) and row T/4 + 8 (the same columns).
 __device__ __forceinline__ void tm_ld_16x16(uint32_t addr, float (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
                : "r"(addr));
+}
+__device__ __forceinline__ void tm_ld_16x32(uint32_t addr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(addr));
 }
 __device__ __forceinline__ void tm_st16u(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -231,20 +239,18 @@ __device__ __forceinline__ void tm_st16u(uint32_t addr, const uint32_t (&r)[16])
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// 16 lanes x 8 columns from all 32 threads: registers 2j and 2j + 1 are
+// 16 lanes x 16 columns from all 32 threads: registers 2j and 2j + 1 are
 // column 4j + T%4 of rows T/4 and T/4 + 8.
-__device__ __forceinline__ void tm_st_16x8(uint32_t addr, const uint32_t (&r)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3])
-               : "memory");
+__device__ __forceinline__ void tm_st_16x16(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
 // Four 8 x 8 matrices of 16-bit elements, transposed: thread T holds elements
 // 2 (T%4) and the next of memory rows, at column T/4.
 __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 __device__ __forceinline__ void stsm4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
@@ -723,26 +729,28 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       // outputs [64 tokens][WR rows], swizzled as the store wants
       const uint32_t out = base + st * L::kStage + L::kV + qd * (C * WR * 2);
 #pragma unroll 1
-      for (int i = 0; i < WR / 16 * 4; ++i) {
-        const int h = i >> 2, q = i & 3;  // 16 rows, 16 tokens
-        const uint32_t from = tw + (static_cast<uint32_t>(16 * h) << 16) + 16 * q;
-        float u[8], y[8];
-        tm_ld_16x16(from + kPtColO1, u);
-        tm_ld_16x16(from + kPtColO2, y);
+      for (int i = 0; i < WR / 16 * 2; ++i) {
+        const int h = i >> 1, q = i & 1;  // 16 rows, 32 tokens
+        const uint32_t from = tw + (static_cast<uint32_t>(16 * h) << 16) + 32 * q;
+        float u[16], y[16];
+        tm_ld_16x32(from + kPtColO1, u);
+        tm_ld_16x32(from + kPtColO2, y);
         const float sa = HALF ? ss[16 * h] : 1.0f, sb = HALF ? ss[16 * h + 8] : 1.0f;
-        wait_ld();
-        uint32_t w[4];
+        float2 d[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 d = *reinterpret_cast<const float2*>(eg + 16 * q + 8 * e);
+        for (int e = 0; e < 4; ++e) d[e] = *reinterpret_cast<const float2*>(eg + 32 * q + 8 * e);
+        wait_ld();
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
           float2 ya = make_float2(y[4 * e], y[4 * e + 1]), yb = make_float2(y[4 * e + 2], y[4 * e + 3]);
-          float2 da = d, db = d;
+          float2 da = d[e], db = d[e];
           if constexpr (HALF) {
-            const float2 k = *reinterpret_cast<const float2*>(sp + 16 * q + 8 * e);
+            const float2 k = *reinterpret_cast<const float2*>(sp + 32 * q + 8 * e);
             ya = __fmul2_rn(k, ya);
             yb = __fmul2_rn(k, yb);
-            da = __fmul2_rn(d, f2(sa));
-            db = __fmul2_rn(d, f2(sb));
+            da = __fmul2_rn(da, f2(sa));
+            db = __fmul2_rn(db, f2(sb));
           }
           const float2 oa = __ffma2_rn(da, make_float2(u[4 * e], u[4 * e + 1]), ya);
           const float2 ob = __ffma2_rn(db, make_float2(u[4 * e + 2], u[4 * e + 3]), yb);
@@ -750,9 +758,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           w[2 * e + 1] = E::narrow2(ob.x, ob.y);
         }
         // matrices: rows 16h.. and 16h + 8.. of two blocks of 8 tokens
-        const int tt = 16 * q + 8 * (m >> 1) + (lane & 7), chunk = 2 * h + (m & 1);
-        const int sw = WR == 32 ? (tt >> 1) & 3 : (tt >> 2) & 1;
-        stsm4_t(out + tt * (2 * WR) + ((chunk ^ sw) << 4), w[0], w[1], w[2], w[3]);
+        const int tt = 32 * q + 8 * (m >> 1) + (lane & 7), chunk = 2 * h + (m & 1);
+        const int sw = WR == 32 ? (tt >> 1) & 3 : (tt >> 2) & 1;  // 16 tokens on, the same
+        const uint32_t to = out + tt * (2 * WR) + ((chunk ^ sw) << 4);
+        stsm4_t(to, w[0], w[1], w[2], w[3]);
+        stsm4_t(to + 16 * (2 * WR), w[4], w[5], w[6], w[7]);
       }
       fence_before();
       fence_async_smem();
@@ -814,40 +824,49 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         fence_async_smem();
       }
-      const float* wt = gate_of(n) + Gate::kW + 32 * half + 2 * (lane % 4);
-      const int m = lane >> 3;  // the matrix whose row address this lane gives to ldmatrix
-      // w v of rows 16h.. and tokens 16q..: pairs of tokens 8j + 2 (T%4) and
-      // the next, [j][0] of row T/4, [j][1] of row T/4 + 8
-      auto values = [&](int h, int q, float2 (&x)[2][2]) {
-        const int col = (MDV / 4) * qd + 16 * h;  // first row of S, a column of v
-        const int t = 32 * half + 16 * q + 8 * (m >> 1) + (lane & 7), chunk = ((col & 63) >> 3) + (m & 1);
-        uint32_t r[2][2];
-        ldsm4_t(s + L::kV + (col >> 6) * L::kPanel + t * 128 + ((chunk ^ (t & 7)) << 4), r[0][0], r[0][1], r[1][0], r[1][1]);
+      // This thread's part of v, all loads before their use: row half h (16
+      // rows), token pairs 8j + 2 (T%4) and the next of the warpgroup's 32,
+      // [..][2j] of row T/4, [..][2j + 1] of row T/4 + 8
+      constexpr int HS = MDV / 64;
+      uint32_t v[HS][8];
+      float2 w[4];
+      {
+        const int m = lane >> 3;  // the matrix whose row address this lane gives to ldmatrix
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 w = *reinterpret_cast<const float2*>(wt + 16 * q + 8 * j);
-          x[j][0] = __fmul2_rn(w, E::widen2(r[j][0]));
-          x[j][1] = __fmul2_rn(w, E::widen2(r[j][1]));
-          if (count < C) {
-            const int tt = 32 * half + 16 * q + 8 * j + 2 * (lane % 4);
-            if (tt >= count) x[j][0].x = x[j][1].x = 0.0f;
-            if (tt + 1 >= count) x[j][0].y = x[j][1].y = 0.0f;
+        for (int h = 0; h < HS; ++h) {
+          const int col = (MDV / 4) * qd + 16 * h;  // first row of S, a column of v
+          const int chunk = ((col & 63) >> 3) + (m & 1), t = 32 * half + 8 * (m >> 1) + (lane & 7);
+          const uint32_t at = s + L::kV + (col >> 6) * L::kPanel + t * 128 + ((chunk ^ (t & 7)) << 4);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            ldsm4_t(at + 16 * q * 128, v[h][4 * q], v[h][4 * q + 1], v[h][4 * q + 2], v[h][4 * q + 3]);
+        }
+        const float* wt = gate_of(n) + Gate::kW + 32 * half + 2 * (lane % 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const float2*>(wt + 8 * j);
+      }
+      if (count < C) {  // tokens that do not count: their weights are 0, their values anything
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int tt = 32 * half + 8 * j + 2 * (lane % 4);
+          const uint32_t keep = tt >= count ? 0u : tt + 1 >= count ? 0xFFFFu : 0xFFFFFFFFu;
+#pragma unroll
+          for (int h = 0; h < HS; ++h) {
+            v[h][2 * j] &= keep;
+            v[h][2 * j + 1] &= keep;
           }
         }
-      };
+      }
+      float u[HS][2];  // fp16: the rows' scales
       if constexpr (HALF) {
-#pragma unroll 1
-        for (int h = 0; h < MDV / 64; ++h) {
-          float m0 = 0.0f, m1 = 0.0f;
-#pragma unroll 1
-          for (int q = 0; q < 2; ++q) {
-            float2 x[2][2];
-            values(h, q, x);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              m0 = fmaxf(m0, fmaxf(fabsf(x[j][0].x), fabsf(x[j][0].y)));
-              m1 = fmaxf(m1, fmaxf(fabsf(x[j][1].x), fabsf(x[j][1].y)));
-            }
+        for (int h = 0; h < HS; ++h) {
+          float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = __fmul2_rn(w[j], E::widen2(v[h][2 * j])), y = __fmul2_rn(w[j], E::widen2(v[h][2 * j + 1]));
+            m0 = fmaxf(m0, fmaxf(fabsf(x.x), fabsf(x.y)));
+            m1 = fmaxf(m1, fmaxf(fabsf(y.x), fabsf(y.y)));
           }
 #pragma unroll
           for (int d = 1; d < 4; d <<= 1) {
@@ -861,34 +880,30 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           }
         }
         if (!pair()) return false;
-      }
-      const uint32_t at = tw + kPtColW + 64 * (n & 1) + 16 * half;
-#pragma unroll 2
-      for (int i = 0; i < MDV / 64 * 2; ++i) {
-        const int h = i >> 1, q = i & 1;
-        float2 x[2][2];
-        values(h, q, x);
-        if constexpr (HALF) {
+#pragma unroll
+        for (int h = 0; h < HS; ++h) {
           const int row = (MDV / 4) * qd + 16 * h + lane / 4;
           float back;
-          const float u0 = row_scale(worst(n & 3, row), back), u1 = row_scale(worst(n & 3, row + 8), back);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            x[j][0] = __fmul2_rn(x[j][0], f2(u0));
-            x[j][1] = __fmul2_rn(x[j][1], f2(u1));
-          }
+          u[h][0] = row_scale(worst(n & 3, row), back);
+          u[h][1] = row_scale(worst(n & 3, row + 8), back);
         }
-        uint32_t hi[4], lo[4];
+      }
+      const uint32_t at = tw + kPtColW + 64 * (n & 1) + 16 * half;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 v = x[j / 2][j % 2];
-          hi[j] = E::narrow2(v.x, v.y);
+      for (int h = 0; h < HS; ++h) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float2 x = __fmul2_rn(w[j / 2], E::widen2(v[h][j]));
+          if constexpr (HALF) x = __fmul2_rn(x, f2(u[h][j % 2]));
+          hi[j] = E::narrow2(x.x, x.y);
           const float2 k = E::widen2(hi[j]);
-          lo[j] = E::narrow2(v.x - k.x, v.y - k.y);
+          const float2 r = __fadd2_rn(x, make_float2(-k.x, -k.y));
+          lo[j] = E::narrow2(r.x, r.y);
         }
-        const uint32_t to = at + (static_cast<uint32_t>(16 * h) << 16) + 8 * q;
-        tm_st_16x8(to, hi);
-        tm_st_16x8(to + 32, lo);
+        const uint32_t to = at + (static_cast<uint32_t>(16 * h) << 16);
+        tm_st_16x16(to, hi);
+        tm_st_16x16(to + 32, lo);
       }
       wait_st();
       fence_before();
@@ -964,19 +979,20 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       float back = 1.0f;
       if constexpr (HALF) row_scale(worst(g & 3, max(irow, 0)), back);
 #pragma unroll
-      for (int q = 0; q < SC / 16; ++q) {
-        float r[16];
-        tm_ld16(tw + kPtColKV + SC * half + 16 * q, r);
+      for (int q = 0; q < SC / 32; ++q) {
+        float r[2][16];
+        tm_ld16(tw + kPtColKV + SC * half + 32 * q, r[0]);
+        tm_ld16(tw + kPtColKV + SC * half + 32 * q + 16, r[1]);
         wait_ld();
-        if (q == SC / 16 - 1) {
+        if (q == SC / 32 - 1) {
           fence_before();
           signal(B::kKvFree);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float2 v = make_float2(r[2 * e], r[2 * e + 1]);
+        for (int e = 0; e < 16; ++e) {
+          float2 v = make_float2(r[e / 8][2 * e % 16], r[e / 8][2 * e % 16 + 1]);
           if constexpr (HALF) v = __fmul2_rn(v, f2(back));
-          S[8 * q + e] = __ffma2_rn(S[8 * q + e], f2(gamma), v);
+          S[16 * q + e] = __ffma2_rn(S[16 * q + e], f2(gamma), v);
         }
       }
       if (chunk_of(g).final) {
