@@ -785,12 +785,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           }
         }
       }
-      // the stage before this one is free once its store has read it
+      // the stage is free once the store has read it
       if (lane == 0) {
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       }
-      if (g > 0) signal(B::kEmpty + (g - 1) % NST);
+      signal(B::kEmpty + st);
     }
   } else {
     // ---- the state into tensor memory, W one chunk ahead, the state's update
@@ -1016,8 +1016,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     }
   }
 
-  // the outputs' stores have read shared memory before it goes
-  if (warp >= 8 && warp < 12 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncwarp();
   if (!ok) *failed = 1;
   __syncthreads();
