@@ -67,18 +67,16 @@ namespace qs {
 #ifndef QS_STREAM_REGS_BDR8
 #define QS_STREAM_REGS_BDR8 200
 #endif
-// The SLOTS instances keep two tiles' places as well, and spill 4 to 26 bytes
-// at 128; INT4 fits 136 (15 warps per SM), INT8 144 (14 warps).
+// The SLOTS instances keep two tiles' places as well and read k from its
+// shared-memory slot, at 128 registers: 16 warps per SM, four for each of its
+// schedulers.
 #ifndef QS_STREAM_REGS_SLOTS
-#define QS_STREAM_REGS_SLOTS 136
-#endif
-#ifndef QS_STREAM_REGS_SLOTS8
-#define QS_STREAM_REGS_SLOTS8 144
+#define QS_STREAM_REGS_SLOTS 128
 #endif
 // Where the tile's key vector lives: 1 reads it from its shared-memory slot
 // at each use, 0 holds it in registers for the tile, -1 (default) does the
-// former for the BDR instances (whose packed-word masks and stored codes
-// take registers of their own) and the latter for the others.
+// former for the BDR and SLOTS instances (whose masks, stored codes and tile
+// places take registers of their own) and the latter for the others.
 #ifndef QS_STREAM_K_SMEM
 #define QS_STREAM_K_SMEM -1
 #endif
@@ -396,8 +394,7 @@ __device__ __forceinline__ long long ld_shared_s64(uint32_t a) {
 // POLICY: 0 dynamic, 1 persistent.
 template <int BITS, int DK, int POLICY, bool BDR, bool DELTA, bool DIAG, bool SLOTS = false>
 __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_REGS_BDR)
-                                : !SLOTS ? QS_STREAM_REGS
-                                : BITS == 8 ? QS_STREAM_REGS_SLOTS8 : QS_STREAM_REGS_SLOTS)
+                                : SLOTS ? QS_STREAM_REGS_SLOTS : QS_STREAM_REGS)
     stream_step_kernel(StreamParams p) {
   static_assert(POLICY == 0 || POLICY == 1, "the yoked policy has its own kernel");
   constexpr int LPR = DK / 32;
@@ -414,7 +411,7 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
   constexpr bool BDR_FLOAT = BDR && POLICY == 0;
   // fixed scales the packed-word BDR and the fast reciprocal take directly
   constexpr float kScaleHi = POLICY == 1 ? 0x1p100f : 0x1p126f;
-  constexpr bool KS = QS_STREAM_K_SMEM < 0 ? BDR : QS_STREAM_K_SMEM != 0;
+  constexpr bool KS = QS_STREAM_K_SMEM < 0 ? BDR || SLOTS : QS_STREAM_K_SMEM != 0;
 
   extern __shared__ __align__(128) unsigned char smem[];
   const int lane = threadIdx.x & 31;
@@ -461,20 +458,29 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
   // ---- SLOTS: the place of a tile's rows.  A skipped entry reads slot 0
   // (in bounds, its values unused) and writes nothing.
   const bool wide = !SLOTS || p.dtype == QS_F32;
-  auto place = [&](unsigned t) -> TileAt {
-    const unsigned entry = t / p.heads, head = t - entry * p.heads;
-    const int sl = __ldg(p.slots + entry);
+  // entry and head of a tile, stepped from tile to tile without a division
+  struct TileNo {
+    unsigned t, entry, head;
+  };
+  auto number = [&](unsigned t) -> TileNo {
+    const unsigned entry = t / p.heads;
+    return {t, entry, t - entry * p.heads};
+  };
+  auto behind = [&](TileNo n) -> TileNo {
+    const bool wrap = n.head + 1 == p.heads;
+    return {n.t + 1, n.entry + wrap, wrap ? 0u : n.head + 1};
+  };
+  auto place = [&](TileNo n) -> TileAt {
+    const int sl = __ldg(p.slots + n.entry);
     TileAt at;
     at.live = sl >= 0 && sl < p.num_slots;
-    const long long first = static_cast<long long>(t) * bpt;  // the tile's first row block in the batch
     at.shift = static_cast<int>(
-        (static_cast<long long>(at.live ? sl : 0) * p.heads + head) * bpt - first);
+        (static_cast<long long>(at.live ? sl : 0) * p.heads + n.head - static_cast<long long>(n.t)) * bpt);
     return at;
   };
-  // the element that row 0 of row block 0 would have in v or o, for tile t
-  auto base_of = [&](unsigned t, long long stride) {
-    const unsigned entry = t / p.heads, head = t - entry * p.heads;
-    return entry * stride + static_cast<long long>(head) * (bpt * RW) - static_cast<long long>(t) * bpt * RW;
+  // the element that row 0 of row block 0 would have in v or o, for tile n
+  auto base_of = [&](TileNo n, long long stride) {
+    return n.entry * stride + (static_cast<long long>(n.head) - static_cast<long long>(n.t)) * (bpt * RW);
   };
   auto load_row_block = [&](BlockIn<BITS>& in, unsigned b, const TileAt& at, long long v0) {
     if constexpr (SLOTS) {
@@ -496,18 +502,19 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
 
   // ---- per-tile vectors: cp.async into the warp's two slots
   const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-  auto stage_tile = [&](unsigned t, int slot) {
+  auto stage_tile = [&](TileNo no, int slot) {
+    const unsigned t = no.t;
     const uint32_t base = slots + slot * L.slot;
     size_t kat = static_cast<size_t>(t) * DK, qat = kat;  // first element of the tile's k and q
     if constexpr (SLOTS) {
       if (lane == 0) {
         long long* at = reinterpret_cast<long long*>(smem + slot * L.slot + L.misc + 16);
-        at[0] = base_of(t, p.v_stride);
-        at[1] = base_of(t, p.o_stride);
+        at[0] = base_of(no, p.v_stride);
+        at[1] = base_of(no, p.o_stride);
       }
-      const unsigned entry = t / p.heads, kh = (t - entry * p.heads) / p.share;
-      kat = entry * static_cast<size_t>(p.k_stride) + kh * DK;
-      qat = entry * static_cast<size_t>(p.q_stride) + kh * DK;
+      const unsigned kh = no.head / p.share;
+      kat = no.entry * static_cast<size_t>(p.k_stride) + kh * DK;
+      qat = no.entry * static_cast<size_t>(p.q_stride) + kh * DK;
       if (!wide && lane < DK / 8) {
         const uint32_t u = base + L.raw + 16 * lane;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(u),
@@ -544,16 +551,19 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
   unsigned tile = b0 / bpt;
   unsigned tile_end = (tile + 1) * bpt;  // first row block of the next tile
   int slot = 0;
-  stage_tile(tile, 0);
+  TileNo no{tile, 0, 0};  // the tile staged last
+  if constexpr (SLOTS) no = number(tile);
+  stage_tile(no, 0);
   cp_async_commit();
-  if (tile_end < b1) stage_tile(tile + 1, 1);
+  TileAt cur{}, nxt{};  // SLOTS: this tile's place and the next one's
+  if constexpr (SLOTS) cur = nxt = place(no);
+  if (tile_end < b1) {
+    no = SLOTS ? behind(no) : TileNo{tile + 1, 0, 0};
+    stage_tile(no, 1);
+    if constexpr (SLOTS) nxt = place(no);
+  }
   cp_async_commit();
 
-  TileAt cur{}, nxt{};  // SLOTS: this tile's place and the next one's
-  if constexpr (SLOTS) {
-    cur = place(tile);
-    nxt = tile_end < b1 ? place(tile + 1) : cur;
-  }
   BlockIn<BITS> A, B;
   auto v_base = [&](int sl) { return SLOTS ? ld_shared_s64(slots + sl * L.slot + L.misc + 16) : 0ll; };
   auto o_base = [&](int sl) { return SLOTS ? ld_shared_s64(slots + sl * L.slot + L.misc + 24) : 0ll; };
@@ -646,8 +656,9 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
           at = nxt;
           v0 = v_base(slot ^ 1);
         } else {  // tiles of one row block
-          at = place(tile + 2);
-          v0 = base_of(tile + 2, p.v_stride);
+          const TileNo two = behind(no);
+          at = place(two);
+          v0 = base_of(two, p.v_stride);
         }
         load_row_block(in, b + 2, at, v0);
       } else {
@@ -836,14 +847,17 @@ __global__ void __maxnreg__(BDR ? (BITS == 8 ? QS_STREAM_REGS_BDR8 : QS_STREAM_R
       slot ^= 1;
       if constexpr (SLOTS) {
         cur = nxt;
-        if (tile_end < b1) nxt = place(tile + 1);
+        if (tile_end < b1) {
+          no = behind(no);
+          nxt = place(no);
+        }
       }
       cp_async_wait<0>();
       // every lane's copies of this tile have landed, and every lane is done
       // with the slot that the next tile's copies overwrite
       __syncwarp();
       enter_tile();
-      if (tile_end < b1) stage_tile(tile + 1, slot ^ 1);
+      if (tile_end < b1) stage_tile(SLOTS ? no : TileNo{tile + 1, 0, 0}, slot ^ 1);
       cp_async_commit();
       if constexpr (SLOTS) __syncwarp();
     }
