@@ -66,6 +66,7 @@ qs_status cache_move(bool write, const qs_config* cfg, int heads, int n, const i
   p.group = cfg->group;
   p.rows = static_cast<unsigned>(heads) * cfg->dv;
   p.blocks = 0;
+  p.two23 = 0x4B000000u;
   cudaError_t e;
   if (cfg->bits == 4)
     e = cfg->dk == 64 ? launch_cache<4, 64>(write, dtype, p, n, stream) : launch_cache<4, 128>(write, dtype, p, n, stream);

@@ -364,20 +364,32 @@ class QState:
 def _dtype_tag(dtype):
     """The qs_dtype of a torch dtype."""
     import torch
-    tag = {torch.float32: QS_F32, torch.float16: QS_F16, torch.bfloat16: QS_BF16}.get(dtype)
-    if tag is None:
+    if dtype is torch.bfloat16:
+        return QS_BF16
+    if dtype is torch.float16:
+        return QS_F16
+    if dtype is not torch.float32:
         raise ValueError(f"float32, float16 or bfloat16 values are wanted, not {dtype}")
-    return tag
+    return QS_F32
 
 
 def _check_tensor(name, t, shape, dtype, device, rows=False):
     """t has this shape, dtype and device, contiguous (`rows`: within each row of dimension 0)."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == device.index and t.is_contiguous():
+        return
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name}: {tuple(shape)} {dtype} is wanted, not {tuple(t.shape)} {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if not (t.is_contiguous() or (rows and t[:1].is_contiguous())):
+    if not (rows and t[:1].is_contiguous()):
         raise ValueError(f"{name} is not contiguous" + (" within a token" if rows else ""))
+
+
+def _current_stream(index: int) -> int:
+    """The handle of a device's current stream."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 class _OnDevice:
@@ -396,8 +408,9 @@ class _OnDevice:
     def _launch(self, what, fn, args, stream):
         import torch
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        handle = stream if isinstance(stream, int) else stream.cuda_stream
+            handle = _current_stream(self.device.index)
+        else:
+            handle = stream if isinstance(stream, int) else stream.cuda_stream
         if torch.cuda.current_device() == self.device.index:
             status = fn(*args, handle)
         else:
