@@ -541,6 +541,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           c = 0;
 #pragma unroll 1
           for (x.chunks = 0; it < a.items && x.chunks == 0; it += gridDim.x) x = item_at(it);
+          if (x.chunks > 0 && x.from != nullptr) {
+            // the item's state toward L2, a few chunks before it is read
+            const char* from = reinterpret_cast<const char*>(x.from + static_cast<size_t>(x.blk) * MDV * DK);
+            const int bytes = min(MDV, p.dv - x.blk * MDV) * DK * 4;
+#pragma unroll 1
+            for (int i = 128 * lane; i < bytes; i += 128 * 32) prefetch_l2(from + i);
+          }
         }
         if (x.chunks > 0) {
           k.t = x.begin + c * C;
