@@ -3,7 +3,7 @@
 #include <mutex>
 
 #include "qstate_check.h"
-#include "qstate_launch.h"
+#include "qstate_launch_impl.cuh"
 #include "qstate_packed_tc.cuh"
 
 namespace {
@@ -74,57 +74,97 @@ bool token_map(CUtensorMap* m, int dtype, const void* base, int width, int heads
 // Rows of S that a CTA of the tensor-core kernel works on.
 int tc_rows(int dv) { return dv <= 64 ? 64 : 128; }
 
+// Two heads of a q/k head share a CTA where their 64 rows each fill its 128
+// lanes together.
+bool two_heads(int dv, int share) { return dv == 64 && share % 2 == 0; }
+
+// CTAs that the heads of one prompt take.
+long long prompt_items(int dv, int heads, int share) {
+  return two_heads(dv, share) ? heads / 2 : static_cast<long long>(heads) * ((dv + tc_rows(dv) - 1) / tc_rows(dv));
+}
+
 // Segments that a prompt is cut into at most: what the SMs offer beyond the
 // heads' row blocks, each at least kMinSegment chunks long.  The SM count is
 // B200's, so that workspace sizes need no device.
 constexpr int kSms = 148, kMinSegment = 4;
-long long max_segments(int dv, int heads, int tokens) {
-  const long long spread = kSms / (static_cast<long long>(heads) * ((dv + tc_rows(dv) - 1) / tc_rows(dv)));
+long long max_segments(int dv, int heads, int share, int tokens) {
+  const long long spread = kSms / prompt_items(dv, heads, share);
   const long long chunks = (static_cast<long long>(tokens) + kPtChunk - 1) / kPtChunk;
   const long long most = chunks / kMinSegment;
   return spread < most ? spread : most;
 }
 
-// Tokens of a segment, or 0 where prompts are not cut: with one segment at
-// most, or with an item for every SM already (two thirds of them: cutting
-// costs a second pass over the keys and values) unless the batch is so long
-// (kLongShare chunks for every SM) that one long prompt among short ones would
-// matter more than the two launches.
+// Tokens of a segment, or 0 where prompts are not cut.  With fewer items than
+// two thirds of the SMs a segment is an SM's share of the chunks.  With more,
+// taking items in falling order of length balances all but a prompt that is
+// longer than that; cutting costs a second pass over the keys and values, so
+// only prompts of twice the share are cut, and only in a batch so long
+// (kLongShare chunks for every SM) that the launches do not matter.
 constexpr int kLongShare = 32;
-int segment_tokens(int dv, int heads, int tokens, int sequences) {
-  const long long n = max_segments(dv, heads, tokens);
+int segment_tokens(int dv, int heads, int share, int tokens, int sequences) {
+  const long long n = max_segments(dv, heads, share, tokens);
   if (n < 2) return 0;
-  const long long tiles = static_cast<long long>(heads) * ((dv + tc_rows(dv) - 1) / tc_rows(dv));
+  const long long tiles = prompt_items(dv, heads, share);
   const long long chunks = (static_cast<long long>(tokens) + kPtChunk - 1) / kPtChunk;
-  if (3 * tiles * sequences > 2 * kSms && chunks * tiles < static_cast<long long>(kLongShare) * kSms) return 0;
-  return static_cast<int>((chunks + n - 1) / n) * kPtChunk;
+  const bool many = 3 * tiles * sequences > 2 * kSms;
+  if (many && chunks * tiles < static_cast<long long>(kLongShare) * kSms) return 0;
+  return static_cast<int>((chunks + n - 1) / n) * kPtChunk * (many ? 2 : 1);
 }
 
-// Bytes of the stored states and decays of n segments (a multiple of 256).
-size_t segment_bytes(int dk, int dv, int heads, long long n, size_t* states) {
-  const size_t s = (static_cast<size_t>(n + 1) * heads * dv * dk * sizeof(float) + 255) / 256 * 256;
-  if (states) *states = s;
-  return s + (static_cast<size_t>(n + 1) * heads * sizeof(float) + 255) / 256 * 256;
+// The workspace: two tickets and a flag, the units' order, and the states and decays of n
+// segments, each from a multiple of 256 bytes on.
+struct PackedSpace {
+  size_t order = 256, states, decays, bytes;
+  PackedSpace(int dk, int dv, int heads, int sequences, long long n) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const size_t stored = n < 2 ? 0 : static_cast<size_t>(n + 1) * heads;
+    states = up(order + (static_cast<size_t>(sequences) + (n < 2 ? 0 : n)) * sizeof(int));
+    decays = up(states + stored * dv * dk * sizeof(float));
+    bytes = up(decays + stored * sizeof(float));
+  }
+};
+
+// Launched as a dependent of the kernel before it (see launch_dependent).
+template <typename K, typename... A>
+cudaError_t launch_next(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <class E, int DK, int MDV>
+template <class E, int DK, int MDV, int NH>
 cudaError_t launch_packed_tc(const PackedParams& p0, int sequences, void* workspace, cudaStream_t stream) {
-  auto kernel = packed_tc_kernel<E, DK, MDV>;
+  auto kernel = packed_tc_kernel<E, DK, MDV, NH>;
+  constexpr int kSmem = PtLayout<DK, MDV, NH>::kBytes;
   static std::once_flag flag;
   cudaError_t err = cudaSuccess;
   std::call_once(flag, [&] {
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PtLayout<DK, MDV>::kBytes);
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   });
   if (err != cudaSuccess) return err;
   PackedTcParams a;
   a.p = p0;
-  a.p.blocks = (p0.dv + MDV - 1) / MDV;
+  a.p.blocks = NH == 2 ? 1 : (p0.dv + MDV - 1) / MDV;
   a.sequences = sequences;
-  a.seg = segment_tokens(p0.dv, p0.heads, p0.tokens, sequences);
+  a.seg = segment_tokens(p0.dv, p0.heads, p0.share, p0.tokens, sequences);
   a.local = false;
-  a.states = a.decays = nullptr;
-  const long long units = sequences + (a.seg > 0 ? p0.tokens / a.seg : 0);
-  a.items = static_cast<int>(units * p0.heads * a.p.blocks);  // < 2^31: batch_fits, and few segments
+  const long long segs = a.seg > 0 ? p0.tokens / a.seg : 0, units = sequences + segs;
+  a.items = static_cast<int>(units * (p0.heads / NH) * a.p.blocks);  // < 2^31: batch_fits, and few segments
+  // laid out for the most segments that the batch's sizes allow, as its bytes were
+  const PackedSpace space(DK, p0.dv, p0.heads, sequences, max_segments(p0.dv, p0.heads, p0.share, p0.tokens));
+  char* const ws = static_cast<char*>(workspace);
+  a.states = reinterpret_cast<float*>(ws + space.states);
+  a.decays = reinterpret_cast<float*>(ws + space.decays);
+  a.order = nullptr;
+  a.ticket = reinterpret_cast<int*>(ws);
   CUtensorMap mq, mk, mv, mo;
   const int qk_heads = p0.heads / p0.share;
   if (!token_map(&mk, E::kTag, p0.k, DK, qk_heads, p0.tokens, p0.k_stride) ||
@@ -136,28 +176,34 @@ cudaError_t launch_packed_tc(const PackedParams& p0, int sequences, void* worksp
     return cudaErrorInvalidValue;
   const int sms = device_sm_count();
   const int grid = a.items < sms ? a.items : sms;
+  a.cut = nullptr;
+  if (a.items > grid) {
+    int* const order = reinterpret_cast<int*>(ws + space.order);
+    err = launch_next(packed_order_kernel, dim3(1), kOrderThreads, 0, stream, a, static_cast<int>(units), order, a.ticket);
+    if (err != cudaSuccess) return err;
+    a.order = order;
+    a.cut = a.ticket + 2;
+  }
   if (a.seg > 0) {
-    size_t states = 0;
-    segment_bytes(DK, p0.dv, p0.heads, p0.tokens / a.seg, &states);
-    a.states = static_cast<float*>(workspace);
-    a.decays = reinterpret_cast<float*>(static_cast<char*>(workspace) + states);
     PackedTcParams first = a;
     first.local = true;
     first.p.o = nullptr;
-    kernel<<<grid, kPtThreads, PtLayout<DK, MDV>::kBytes, stream>>>(mq, mk, mv, mo, first);
+    first.ticket = a.ticket + 1;
+    err = launch_next(kernel, dim3(grid), kPtThreads, kSmem, stream, mq, mk, mv, mo, first);
+    if (err != cudaSuccess) return err;
     const int quads = (p0.dv * DK / 4 + kJoinThreads - 1) / kJoinThreads;
-    packed_join_kernel<DK><<<dim3(static_cast<unsigned>(quads) * sequences, p0.heads), kJoinThreads, 0, stream>>>(a, quads);
+    err = launch_next(packed_join_kernel<DK>, dim3(static_cast<unsigned>(quads) * sequences, p0.heads), kJoinThreads, 0, stream,
+                      a, quads);
+    if (err != cudaSuccess) return err;
   }
-  kernel<<<grid, kPtThreads, PtLayout<DK, MDV>::kBytes, stream>>>(mq, mk, mv, mo, a);
-  return cudaGetLastError();
+  return launch_next(kernel, dim3(grid), kPtThreads, kSmem, stream, mq, mk, mv, mo, a);
 }
 
-template <class E>
-cudaError_t launch_tc(int dk, const PackedParams& p, int sequences, void* ws, cudaStream_t stream) {
-  const bool small = tc_rows(p.dv) == 64;
-  if (dk == 64)
-    return small ? launch_packed_tc<E, 64, 64>(p, sequences, ws, stream) : launch_packed_tc<E, 64, 128>(p, sequences, ws, stream);
-  return small ? launch_packed_tc<E, 128, 64>(p, sequences, ws, stream) : launch_packed_tc<E, 128, 128>(p, sequences, ws, stream);
+template <class E, int DK>
+cudaError_t launch_tc(const PackedParams& p, int sequences, void* ws, cudaStream_t stream) {
+  if (two_heads(p.dv, p.share)) return launch_packed_tc<E, DK, 128, 2>(p, sequences, ws, stream);
+  return tc_rows(p.dv) == 64 ? launch_packed_tc<E, DK, 64, 1>(p, sequences, ws, stream)
+                             : launch_packed_tc<E, DK, 128, 1>(p, sequences, ws, stream);
 }
 
 }  // namespace
@@ -169,8 +215,11 @@ qs_status qstate_prefill_packed_workspace(const qs_config* cfg, const qs_tokens*
   qs_config c;
   const qs_status st = check_packed(cfg, batch, sequences, &c);
   if (st != QS_OK) return st;
-  const long long n = batch->dtype == QS_F32 ? 0 : max_segments(c.dv, batch->heads, batch->tokens);
-  if (bytes) *bytes = n < 2 ? 0 : segment_bytes(c.dk, c.dv, batch->heads, n, nullptr);
+  if (bytes)
+    *bytes = batch->dtype == QS_F32
+                 ? 0
+                 : PackedSpace(c.dk, c.dv, batch->heads, sequences,
+                               max_segments(c.dv, batch->heads, batch->heads / batch->qk_heads, batch->tokens)).bytes;
   return QS_OK;
 }
 
@@ -223,8 +272,10 @@ qs_status qstate_prefill_packed(const qs_config* cfg, const qs_tokens* batch, in
   p.blocks = 0;
   cudaError_t e;
   if (batch->dtype != QS_F32 && any) {
-    e = batch->dtype == QS_F16 ? launch_tc<F16>(c.dk, p, sequences, workspace, stream)
-                                  : launch_tc<BF16>(c.dk, p, sequences, workspace, stream);
+#define QS_TC(E) (c.dk == 64 ? launch_tc<E, 64>(p, sequences, workspace, stream) \
+                             : launch_tc<E, 128>(p, sequences, workspace, stream))
+    e = batch->dtype == QS_F16 ? QS_TC(F16) : QS_TC(BF16);
+#undef QS_TC
     return from_cuda(e);
   }
 #define QS_REC(DK) (batch->dtype == QS_F32 ? launch_recurrent<DK, F32>(p, sequences, stream) \

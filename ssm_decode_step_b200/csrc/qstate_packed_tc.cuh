@@ -58,8 +58,14 @@ namespace qs {
 
 constexpr int kPtThreads = 640;
 constexpr int kPtChunk = 64;
-// tensor-memory columns
-constexpr uint32_t kPtColScore = 0, kPtColO1 = 64, kPtColO2 = 128, kPtColKV = 192, kPtColS = 320, kPtColW = 384;
+// Tensor-memory columns with NH heads in an item: two heads' O2 lie side by
+// side, and W then has one buffer instead of two.
+template <int NH>
+struct PtCol {
+  static constexpr uint32_t kScore = 0, kO1 = 64, kO2 = 128, kKV = kO2 + 64 * NH, kS = kKV + 128, kW = kS + 64;
+  static constexpr int kWBufs = NH == 2 ? 1 : 2;
+  static_assert(kW + 64 * kWBufs == 512, "all columns are used");
+};
 constexpr float kPtReset = 0x1p-120f;
 
 // Few prompts and heads leave most SMs without an item.  Then a prompt longer
@@ -80,52 +86,78 @@ struct PackedTcParams {
   bool local;     // the first of the three launches
   float* states;  // [tokens / seg + 1][heads][Dv][Dk]
   float* decays;  // [tokens / seg + 1][heads]: the segment's whole decay
+  // More items than CTAs: the CTAs take them from a ticket counter, units in
+  // falling order of length (packed_order_kernel).  Null: one item a CTA.
+  const int* order;  // [units]
+  int* ticket;
+  const int* cut;    // whether any prompt is cut, where `order` was made (null: assume so)
 };
+
+// Segment `seg` of prompt `seq` is unit number `unit` of the work; seg < 0, or
+// not below the prompt's segments: the unit is empty.
+__device__ __forceinline__ void unit_at(const PackedTcParams& a, int unit, int& seq, int& seg) {
+  seq = unit;
+  seg = 0;
+  if (a.seg == 0) return;
+  auto first = [&](int i) { return min(max(__ldg(a.p.starts + i), 0), a.p.tokens) / a.seg + i; };
+  int lo = 0, hi = a.sequences - 1;
+#pragma unroll 1
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first(mid) <= unit) lo = mid; else hi = mid - 1;
+  }
+  seq = lo;
+  seg = unit - first(lo);
+}
 
 __device__ __forceinline__ int prompt_segments(int begin, int end, int seg) {
   return end > begin ? (end - begin + seg - 1) / seg : 1;
 }
 
 // Shared memory of a CTA (byte offsets from a 1024-byte boundary).
-template <int DK, int MDV>
+template <int DK, int MDV, int NH>
 struct PtLayout {
   static constexpr int kPanel = kPtChunk * 128;  // 64 tokens x 64 columns, 128-byte swizzled
   static constexpr int kQ = 0, kK = DK / 64 * kPanel, kV = 2 * kK, kStage = kV + MDV / 64 * kPanel;
-  static constexpr int kStages = DK == 128 ? 4 : 5;
-  static constexpr int kP = kStages * kStage;           // two buffers of 64 x 64
-  static constexpr int kGate = kP + 2 * kPanel;         // per stage, see Gate
-  static constexpr int kGateSlot = 6 * 256 + 128;
-  static constexpr int kScaleS = kGate + kStages * kGateSlot;  // fp16: 2 x 128 row scales of S
-  static constexpr int kScaleP = kScaleS + 1024;               // fp16: 4 x 64 row scales of P
-  static constexpr int kMax = kScaleP + 1024;                  // fp16: 6 x 2 x 128 row maxima, 4 of W and 2 of S
+  static constexpr int kStages = DK == 128 ? (NH == 2 ? 3 : 4) : NH == 2 ? 4 : 5;
+  static constexpr int kGates = DK == 128 && NH == 1 ? 5 : 8;  // ring of gate slots, longer than the stages'
+  static constexpr int kP = kStages * kStage;           // two buffers of 64 x 64 a head
+  static constexpr int kGate = kP + 2 * NH * kPanel;         // see Gate
+  static constexpr int kGateSlot = NH * 6 * 256 + 128;
+  static constexpr int kScaleS = kGate + kGates * kGateSlot;  // fp16: 2 x 128 row scales of S
+  static constexpr int kScaleP = kScaleS + 1024;               // fp16: 4 x 64 row scales of P a head
+  static constexpr int kMax = kScaleP + 1024 * NH;                  // fp16: 6 x 2 x 128 row maxima, 4 of W and 2 of S
   static constexpr int kSeen = kMax + 6144;                    // chunks whose gates are being loaded
   static constexpr int kBars = kSeen + 256;
-  static constexpr int kBytes = kBars + 320 + 1024;
+  static constexpr int kBytes = kBars + 512 + 1024;
 };
 
-// A chunk's factors, in floats from its gate slot: the integers and
-// fractions of G, beta, W's weights 2^{G_C - G} beta, 2^G, the first token
-// that a token still sees (int), and what the chunk is (Chunk).
+// A chunk's factors, in floats from its gate slot, for each head kHead apart:
+// the integers and fractions of G, beta, W's weights 2^{G_C - G} beta, 2^G and
+// the first token that a token still sees (int).  Behind the last head's, what
+// the chunk is (Chunk).
 struct Gate {
-  static constexpr int kInt = 0, kFrac = 64, kBeta = 128, kW = 192, kDecay = 256, kFirst = 320, kChunk = 384;
+  static constexpr int kInt = 0, kFrac = 64, kBeta = 128, kW = 192, kDecay = 256, kFirst = 320, kHead = 384;
 };
 struct Chunk {
   const float* from;  // first chunk of an item: the head's state before it (null: zeros)
   float* to;          // last chunk of an item: where the state goes (null: nowhere)
-  float* decay;       // last chunk of an item: where the item's whole decay goes (null: nowhere)
-  float last;         // 2^{G_C}
+  float* decay;       // last chunk of an item: where its heads' whole decays go (null: nowhere)
+  float last[2];      // 2^{G_C} of each head
   int t, n;           // first token, tokens (0: the state alone); n < 0: no more chunks
   int head, row;      // head, first row of S
   int first, final;   // of its item
 };
 
 // mbarriers, 8 bytes each
-template <int NST>
+template <int NST, int NG>
 struct PtBars {
-  static constexpr int kFull = 0, kEmpty = NST, kGateFull = 2 * NST, kGateFree = 3 * NST, kScFull = 4 * NST,
+  static constexpr int kFull = 0, kEmpty = NST, kGateFull = 2 * NST, kGateFree = kGateFull + NG,
+                       kScFull = kGateFree + NG,
                        kScFree = kScFull + 1, kPFull = kScFull + 2, kPFree = kPFull + 2, kWFull = kPFree + 2,
                        kKvFull = kWFull + 2, kKvFree = kKvFull + 1, kSFull = kKvFree + 1, kO1Done = kSFull + 1,
-                       kOFull = kO1Done + 1, kOFree = kOFull + 1, kPair = kOFree + 1, kCount = kPair + 1;
+                       kOFull = kO1Done + 1, kOFree = kOFull + 1, kPair = kOFree + 1, kItemFull = kPair + 1,
+                       kItemFree = kItemFull + 4, kCount = kItemFree + 4;
 };
 
 namespace pt {
@@ -284,16 +316,23 @@ __device__ __forceinline__ float row_scale(float m, float& back) {
 // CTAs whose wait gave up since the library was loaded.
 static __device__ unsigned int packed_timeouts = 0;
 
-template <class E, int DK, int MDV>
+// NH = 2 (Dv = 64, MDV = 128): an item is two neighbouring heads of one q/k
+// head, whose rows fill the 128 lanes together; the scores are shared, P and
+// the gates are each head's own, and O2's contraction runs over both heads'
+// columns (a row's other head's are not read).
+template <class E, int DK, int MDV, int NH>
 __global__ void __launch_bounds__(kPtThreads, 1)
     packed_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
                      const PackedTcParams a) {
   using namespace pt;
-  using L = PtLayout<DK, MDV>;
+  using L = PtLayout<DK, MDV, NH>;
+  using Col = PtCol<NH>;
+  static_assert(NH == 1 || MDV == 128, "two heads fill the lanes");
   constexpr int NST = L::kStages;
-  using B = PtBars<NST>;
-  static_assert(B::kCount * 8 + 8 <= 320, "barriers fit their space");
+  constexpr int NG = L::kGates;
+  using B = PtBars<NST, NG>;
+  static_assert(B::kCount * 8 + 24 <= 512, "barriers fit their space");
   constexpr int C = kPtChunk;
   constexpr bool HALF = E::kTag == QS_F16;
   using T = typename E::T;
@@ -303,6 +342,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   unsigned char* const sm = raw + (base - saddr(raw));
   uint32_t* const tslot = reinterpret_cast<uint32_t*>(sm + L::kBars + 8 * B::kCount);
   volatile uint32_t* const failed = tslot + 1;
+  volatile int* const queue = reinterpret_cast<volatile int*>(tslot + 2);  // items under way
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int qd = warp & 3;
   const bool outputs = p.o != nullptr;
@@ -317,6 +357,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     for (int s = 0; s < NST; ++s) {
       bar_init(bar(B::kFull + s), 1);
       bar_init(bar(B::kEmpty + s), outputs ? 4 + 8 : 8);       // the outputs' warps, the state's warps
+    }
+    for (int s = 0; s < NG; ++s) {
       bar_init(bar(B::kGateFull + s), 1);
       bar_init(bar(B::kGateFree + s), outputs ? 4 + 4 + 8 : 8);  // its readers
     }
@@ -334,13 +376,21 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     bar_init(bar(B::kOFull), 1);
     bar_init(bar(B::kOFree), 4);
     bar_init(bar(B::kPair), 8);
+    for (int i = 0; i < 4; ++i) {
+      bar_init(bar(B::kItemFull + i), 1);
+      bar_init(bar(B::kItemFree + i), 1);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     *failed = 0;
   }
+  // From here on the next kernel of the stream may be scheduled; what the one
+  // before it wrote is not read before grid_dep_wait.
+  grid_dep_launch();
   // P above the diagonal blocks stays zero
-  for (int i = tid; i < 2 * L::kPanel / 16; i += kPtThreads)
+  for (int i = tid; i < 2 * NH * L::kPanel / 16; i += kPtThreads)
     *reinterpret_cast<uint4*>(sm + L::kP + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
   fence_async_smem();
+  grid_dep_wait();
   fence_before();
   __syncthreads();
   fence_after();
@@ -360,9 +410,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     __syncwarp();
     if (lane == 0) arrive(bar(b));
   };
-  auto gate_of = [&](int n) { return reinterpret_cast<float*>(sm + L::kGate + (n % NST) * L::kGateSlot); };
+  auto gate_of = [&](int n) { return reinterpret_cast<float*>(sm + L::kGate + (n % NG) * L::kGateSlot); };
   auto chunk_of = [&](int n) -> const volatile Chunk& {
-    return *reinterpret_cast<const volatile Chunk*>(gate_of(n) + Gate::kChunk);
+    return *reinterpret_cast<const volatile Chunk*>(gate_of(n) + NH * Gate::kHead);
   };
 
   struct Item {
@@ -374,22 +424,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   auto item_at = [&](int it) {
     Item x;
     x.blk = it % p.blocks;
-    const int r = it / p.blocks;
-    int seq = r / p.heads, seg = 0;
-    x.head = r - seq * p.heads;
+    const int r = it / p.blocks, heads = p.heads / NH;
+    int seq = r / heads, seg = 0;
+    x.head = (r - seq * heads) * NH;
     const size_t tile = static_cast<size_t>(p.dv) * DK;
-    if (a.seg > 0) {
-      const int unit = seq;
-      auto first = [&](int i) { return min(max(__ldg(p.starts + i), 0), p.tokens) / a.seg + i; };
-      int lo = 0, hi = a.sequences - 1;
-#pragma unroll 1
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first(mid) <= unit) lo = mid; else hi = mid - 1;
-      }
-      seq = lo;
-      seg = unit - first(lo);
-    }
+    unit_at(a, a.order == nullptr ? seq : __ldg(a.order + seq), seq, seg);
     prompt_bounds(p.starts, seq, p.tokens, x.begin, x.end);
     const size_t at = (static_cast<size_t>(seq) * p.heads + x.head) * tile;
     x.from = p.S0 == nullptr ? nullptr : p.S0 + at;
@@ -420,19 +459,33 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   };
   const int irow = tc_row<MDV>(qd, lane);  // row of S of this lane
 
-  // Registers: 5 warpgroups of 96 at launch (480 a thread slot); the state's
-  // two take 136 each, the others give up what they do not need: 64 + 64 + 80 +
-  // 2 * 136 = 480.
+  const int items = a.local && a.cut != nullptr && __ldg(a.cut) == 0 ? 0 : a.items;
+  const int rows = NH * p.dv;                           // rows of S of an item's heads
+  const int mine = NH == 2 ? qd >> 1 : 0;               // this warp's rows are this head's
+  const int hrow = (MDV / 4) * qd - 64 * mine;          // and start at this row of it
+
+  // Registers: 5 warpgroups of 96 at launch, 480 a thread slot, which the roles
+  // share out anew: the single warps, P, the outputs, and the state's two.
+  constexpr int kRegs0 = NH == 1 ? 64 : HALF ? 72 : 80, kRegsP = HALF ? 80 : 64, kRegsO = NH == 2 && HALF ? 72 : 80,
+                kRegsS = NH == 1 && !HALF ? 136 : 128;
+  static_assert(kRegs0 + kRegsP + kRegsO + 2 * kRegsS <= 480, "the launch's registers");
   bool ok = true;
   int g = 0;  // chunks so far, over all items of this CTA
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs0));
     if (warp == 0) {
       // ---- loads
       if (lane == 0) {
+        int k = 0;  // items so far
 #pragma unroll 1
-        for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+        for (int it = blockIdx.x;; ++k) {
+          // the item to the warp that describes its chunks; items: no more
+          if (!(ok = wait(B::kItemFree + k % 4, k / 4 - 1))) break;
+          queue[k % 4] = it;
+          arrive(bar(B::kItemFull + k % 4));
+          if (it >= items) break;
           const Item x = item_at(it);
+          it = a.order == nullptr ? items : static_cast<int>(gridDim.x) + atomicAdd(a.ticket, 1);
 #pragma unroll 1
           for (int c = 0; c < x.chunks; ++c, ++g) {
             const int st = g % NST;
@@ -447,8 +500,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
 #pragma unroll
             for (int i = 0; i < MDV / 64; ++i)
-              tma_load3(s + L::kV + i * L::kPanel, &mv, x.blk * MDV + 64 * i, x.head, t, f);
+              tma_load3(s + L::kV + i * L::kPanel, &mv, NH == 2 ? 0 : x.blk * MDV + 64 * i, NH == 2 ? x.head + i : x.head, t, f);
           }
+          if (!ok) break;
         }
         // after a timeout: the copies in flight land before the CTA leaves
         if (!ok)
@@ -457,20 +511,20 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     } else if (warp == 1) {
       // ---- contractions: the outputs' two.  The whole warp runs the loop, so
       // that addresses stay uniform; one lane issues.
-      constexpr uint32_t id_o1 = idesc<E>(MDV, C, false, false), id_o2 = idesc<E>(MDV, C, true, false);
+      constexpr uint32_t id_o1 = idesc<E>(MDV, C, false, false), id_o2 = idesc<E>(MDV, NH * C, true, false);
       // descriptors of stage 0; a byte offset adds a sixteenth of itself
       const uint64_t dq = desc128(base + L::kQ, 16), dv = desc128(base + L::kV, L::kPanel), dp = desc128(base + L::kP, 16);
 #pragma unroll 1
       for (; outputs; ++g) {
-        const uint32_t s = (g % NST) * (L::kStage / 16), pb = (g & 1) * (L::kPanel / 16);
-        if (!(ok = wait_all(B::kGateFull + g % NST, g / NST)) || chunk_of(g).n < 0) break;
+        const uint32_t s = (g % NST) * (L::kStage / 16), pb = (g & 1) * (NH * L::kPanel / 16);
+        if (!(ok = wait_all(B::kGateFull + g % NG, g / NG)) || chunk_of(g).n < 0) break;
         // the state's warps have waited for this stage's loads
         if (!(ok = wait_all(B::kSFull, g) && wait_all(B::kOFree, g - 1))) break;
         fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < DK / 16; ++k)
-            mma16_ts(tm + kPtColO1, tm + kPtColS + 8 * k, dq + (s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16), id_o1, k > 0);
+            mma16_ts(tm + Col::kO1, tm + Col::kS + 8 * k, dq + (s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16), id_o1, k > 0);
           mma_commit(bar(B::kO1Done));
         }
         __syncwarp();
@@ -479,7 +533,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < C / 16; ++k)
-            mma16_ss(tm + kPtColO2, dv + (s + k * (2048 / 16)), dp + (pb + 2 * k), id_o2, k > 0);
+            mma16_ss(tm + Col::kO2, dv + (s + k * (2048 / 16)), dp + (pb + 2 * k), id_o2, k > 0);
           mma_commit(bar(B::kOFull));
           mma_commit(bar(B::kPFree + (g & 1)));
         }
@@ -491,7 +545,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const uint64_t dq = desc128(base + L::kQ, 16), dk = desc128(base + L::kK, 16), dkt = desc128(base + L::kK, L::kPanel);
 #pragma unroll 1
       for (int n = 0;; ++n) {
-        if (!(ok = wait_all(B::kGateFull + n % NST, n / NST))) break;
+        if (!(ok = wait_all(B::kGateFull + n % NG, n / NG))) break;
         const bool more = chunk_of(n).n >= 0;
         if (outputs && more) {
           if (!(ok = wait_all(B::kFull + n % NST, n / NST) && wait_all(B::kScFree, n - 1))) break;
@@ -501,7 +555,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
             for (int k = 0; k < DK / 16; ++k) {
               const uint32_t off = s + ((k / 4) * L::kPanel + (k % 4) * 32) / 16;
-              mma16_ss(tm + kPtColScore, dq + off, dk + off, id_sc, k > 0);
+              mma16_ss(tm + Col::kScore, dq + off, dk + off, id_sc, k > 0);
             }
             mma_commit(bar(B::kScFull));
           }
@@ -509,13 +563,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         if (n > 0) {
           g = n - 1;
-          if (!(ok = wait_all(B::kWFull + (g & 1), g >> 1) && wait_all(B::kKvFree, g - 1))) break;
+          if (!(ok = wait_all(B::kWFull + g % Col::kWBufs, g / Col::kWBufs) && wait_all(B::kKvFree, g - 1))) break;
           fence_after();
           if (elect_one()) {
-            const uint32_t s = (g % NST) * (L::kStage / 16), w = tm + kPtColW + 64 * (g & 1);
+            const uint32_t s = (g % NST) * (L::kStage / 16), w = tm + Col::kW + 64 * (g % Col::kWBufs);
 #pragma unroll
             for (int k = 0; k < C / 8; ++k)  // 4 steps of W's value, 4 of its rounding error
-              mma16_ts(tm + kPtColKV, w + 8 * k, dkt + (s + (k % 4) * (2048 / 16)), id_kv, k > 0);
+              mma16_ts(tm + Col::kKV, w + 8 * k, dkt + (s + (k % 4) * (2048 / 16)), id_kv, k > 0);
             mma_commit(bar(B::kKvFull));
           }
           __syncwarp();
@@ -528,23 +582,32 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       // alone in their sector, so they take a full trip to memory)
       constexpr int kAhead = 2;
       struct Gates {
-        float a0 = 1.0f, a1 = 1.0f, b0 = 0.0f, b1 = 0.0f;
+        float a0[NH], a1[NH], b0[NH], b1[NH];
       };
       Chunk* const seen = reinterpret_cast<Chunk*>(sm + L::kSeen);  // the chunks whose loads are in flight
-      int it = blockIdx.x, c = 0, loaded = 0;
+      int taken = 0, c = 0, loaded = 0;
+      bool done = false;
       Item x{};
       auto load = [&]() -> Gates {  // the next chunk's
         Gates r;
+#pragma unroll
+        for (int e = 0; e < NH; ++e) r.a0[e] = r.a1[e] = 1.0f, r.b0[e] = r.b1[e] = 0.0f;
         Chunk k;
         k.n = -1;
         if (c == x.chunks) {
           c = 0;
 #pragma unroll 1
-          for (x.chunks = 0; it < a.items && x.chunks == 0; it += gridDim.x) x = item_at(it);
+          for (x.chunks = 0; !done && x.chunks == 0; ++taken) {
+            done = !wait_all(B::kItemFull + taken % 4, taken / 4);
+            const int it = queue[taken % 4];
+            signal(B::kItemFree + taken % 4);
+            done = done || it >= items;
+            if (!done) x = item_at(it);
+          }
           if (x.chunks > 0 && x.from != nullptr) {
             // the item's state toward L2, a few chunks before it is read
             const char* from = reinterpret_cast<const char*>(x.from + static_cast<size_t>(x.blk) * MDV * DK);
-            const int bytes = min(MDV, p.dv - x.blk * MDV) * DK * 4;
+            const int bytes = min(MDV, rows - x.blk * MDV) * DK * 4;
 #pragma unroll 1
             for (int i = 128 * lane; i < bytes; i += 128 * 32) prefetch_l2(from + i);
           }
@@ -554,8 +617,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           k.n = min(x.end - k.t, C);
           const size_t at = static_cast<size_t>(k.t + lane) * p.heads + x.head;
           const size_t at1 = at + static_cast<size_t>(32) * p.heads;
-          if (lane < k.n) r.a0 = __ldg(p.alpha + at), r.b0 = __ldg(p.beta + at);
-          if (lane + 32 < k.n) r.a1 = __ldg(p.alpha + at1), r.b1 = __ldg(p.beta + at1);
+#pragma unroll
+          for (int e = 0; e < NH; ++e) {
+            if (lane < k.n) r.a0[e] = __ldg(p.alpha + at + e), r.b0[e] = __ldg(p.beta + at + e);
+            if (lane + 32 < k.n) r.a1[e] = __ldg(p.alpha + at1 + e), r.b1[e] = __ldg(p.beta + at1 + e);
+          }
           k.head = x.head;
           k.row = x.blk * MDV;
           k.first = c == 0;
@@ -577,135 +643,164 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
         for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
         ahead[kAhead - 1] = load();
-        const bool z0 = now.a0 < kPtReset, z1 = now.a1 < kPtReset;
         // the running sum of log2(alpha), in units of 2^-32
         auto fixed = [](float v) { return __float2ll_rn(v * 0x1p32f); };
         auto real = [](long long v) { return __ll2float_rn(v) * 0x1p-32f; };
-        long long x0 = z0 ? 0 : fixed(log2f(now.a0)), x1 = z1 ? 0 : fixed(log2f(now.a1));
+        float last[NH], bad[NH];
+        long long x0[NH], x1[NH], gc[NH];
+        int r0[NH], r1[NH], rc[NH];
+#pragma unroll
+        for (int e = 0; e < NH; ++e) {
+          const bool z0 = now.a0[e] < kPtReset, z1 = now.a1[e] < kPtReset;
+          x0[e] = z0 ? 0 : fixed(log2f(now.a0[e]));
+          x1[e] = z1 ? 0 : fixed(log2f(now.a1[e]));
+          // the last reset at or before a token: what lies before it is forgotten
+          const uint32_t m0 = __ballot_sync(0xffffffffu, z0), m1 = __ballot_sync(0xffffffffu, z1);
+          const uint32_t le = 0xffffffffu >> (31 - lane);
+          r0[e] = (m0 & le) ? 31 - __clz(m0 & le) : -1;
+          const int r31 = m0 ? 31 - __clz(m0) : -1;
+          r1[e] = (m1 & le) ? 63 - __clz(m1 & le) : r31;
+          rc[e] = m1 ? 63 - __clz(m1) : r31;
+          // NaN and infinite decays (which the fixed point cannot hold) spoil
+          // their prompt from here on, as they should
+          bad[e] = __any_sync(0xffffffffu, !(now.a0[e] < INFINITY && now.a1[e] < INFINITY)) ? NAN : 0.0f;
+        }
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-          const long long y0 = __shfl_up_sync(0xffffffffu, x0, d), y1 = __shfl_up_sync(0xffffffffu, x1, d);
-          if (lane >= d) {
-            x0 += y0;
-            x1 += y1;
+#pragma unroll
+          for (int e = 0; e < NH; ++e) {
+            const long long y0 = __shfl_up_sync(0xffffffffu, x0[e], d), y1 = __shfl_up_sync(0xffffffffu, x1[e], d);
+            if (lane >= d) {
+              x0[e] += y0;
+              x1[e] += y1;
+            }
           }
         }
-        x1 += __shfl_sync(0xffffffffu, x0, 31);
-        const long long gc = __shfl_sync(0xffffffffu, x1, 31);
-        // NaN and infinite decays (which the fixed point cannot hold) spoil
-        // their prompt from here on, as they should
-        const float bad = __any_sync(0xffffffffu, !(now.a0 < INFINITY && now.a1 < INFINITY)) ? NAN : 0.0f;
-        // the last reset at or before a token: what lies before it is forgotten
-        const uint32_t m0 = __ballot_sync(0xffffffffu, z0), m1 = __ballot_sync(0xffffffffu, z1);
-        const uint32_t le = 0xffffffffu >> (31 - lane);
-        const int r0 = (m0 & le) ? 31 - __clz(m0 & le) : -1;
-        const int r31 = m0 ? 31 - __clz(m0) : -1;
-        const int r1 = (m1 & le) ? 63 - __clz(m1 & le) : r31;
-        const int rc = m1 ? 63 - __clz(m1) : r31;
-        if (!(ok = wait_all(B::kGateFree + g % NST, g / NST - 1))) break;
-        float* f = gate_of(g);
-        int* first = reinterpret_cast<int*>(f + Gate::kFirst);
-        auto put = [&](int t, long long x, float be, int r) {
-          f[Gate::kInt + t] = static_cast<float>(static_cast<int>(x >> 32));
-          f[Gate::kFrac + t] = __uint2float_rn(static_cast<uint32_t>(x)) * 0x1p-32f + bad;
-          f[Gate::kBeta + t] = be;
-          f[Gate::kW + t] = t >= rc ? be * ex2(real(gc - x)) : 0.0f;
-          f[Gate::kDecay + t] = r < 0 ? exp2f(real(x)) : 0.0f;
-          first[t] = max(r, 0);
-        };
-        put(lane, x0, now.b0, r0);
-        put(lane + 32, x1, now.b1, r1);
+#pragma unroll
+        for (int e = 0; e < NH; ++e) {
+          x1[e] += __shfl_sync(0xffffffffu, x0[e], 31);
+          gc[e] = __shfl_sync(0xffffffffu, x1[e], 31);
+        }
+        if (!(ok = wait_all(B::kGateFree + g % NG, g / NG - 1))) break;
+#pragma unroll
+        for (int e = 0; e < NH; ++e) {
+          float* f = gate_of(g) + e * Gate::kHead;
+          int* first = reinterpret_cast<int*>(f + Gate::kFirst);
+          auto put = [&](int t, long long x, float be, int r) {
+            f[Gate::kInt + t] = static_cast<float>(static_cast<int>(x >> 32));
+            f[Gate::kFrac + t] = __uint2float_rn(static_cast<uint32_t>(x)) * 0x1p-32f + bad[e];
+            f[Gate::kBeta + t] = be;
+            f[Gate::kW + t] = t >= rc[e] ? be * ex2(real(gc[e] - x)) : 0.0f;
+            f[Gate::kDecay + t] = r < 0 ? exp2f(real(x)) : 0.0f;
+            first[t] = max(r, 0);
+          };
+          put(lane, x0[e], now.b0[e], r0[e]);
+          put(lane + 32, x1[e], now.b1[e], r1[e]);
+          last[e] = (rc[e] < 0 ? exp2f(real(gc[e])) : 0.0f) + bad[e];
+        }
         __syncwarp();
         const int n = seen[g % (kAhead + 1)].n;
         if (lane == 0) {
           Chunk k = seen[g % (kAhead + 1)];
-          k.last = (rc < 0 ? exp2f(real(gc)) : 0.0f) + bad;
-          *reinterpret_cast<Chunk*>(f + Gate::kChunk) = k;
+#pragma unroll
+          for (int e = 0; e < NH; ++e) k.last[e] = last[e];
+          *reinterpret_cast<Chunk*>(gate_of(g) + NH * Gate::kHead) = k;
         }
-        signal(B::kGateFull + g % NST);
+        signal(B::kGateFull + g % NG);
         if (n < 0) break;
       }
     }
   } else if (warp < 8) {
     // ---- P
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsP));
     const int t0 = 16 * qd + lane / 4, t1 = t0 + 8, cc = 2 * (lane % 4);  // this thread's rows, and columns of 8
 #pragma unroll 1
     for (; outputs; ++g) {
       const int st = g % NST, buf = g & 1;
-      if (!(ok = wait_all(B::kGateFull + st, g / NST)) || chunk_of(g).n < 0) break;
+      if (!(ok = wait_all(B::kGateFull + g % NG, g / NG)) || chunk_of(g).n < 0) break;
       if (!(ok = wait_all(B::kPFree + buf, (g >> 1) - 1) && wait_all(B::kScFull, g))) break;
       fence_after();
-      const float* f = gate_of(g);
-      const int* first = reinterpret_cast<const int*>(f + Gate::kFirst);
-      const float2 i0 = f2(f[Gate::kInt + t0]), i1 = f2(f[Gate::kInt + t1]);
-      const float2 f0 = f2(f[Gate::kFrac + t0]), f1 = f2(f[Gate::kFrac + t1]);
-      const int l0 = first[t0], l1 = first[t1];
-      const unsigned w0 = t0 - l0, w1 = t1 - l1;
-      // the decayed scores of columns 8j + cc and the next, in place
-      auto decayed = [&](int j, float (&r)[8], int i) {
-        const int s = 8 * j + cc;
-        auto at = [&](int k) { return *reinterpret_cast<const float2*>(f + k + s); };
-        const float2 is = at(Gate::kInt), fs = at(Gate::kFrac), be = at(Gate::kBeta);
-        const float2 ni = make_float2(-is.x, -is.y), nf = make_float2(-fs.x, -fs.y);
-        auto two = [&](float& a0, float& a1, float2 it, float2 ft, int l, unsigned w) {
-          const float2 d = __fadd2_rn(__fadd2_rn(it, ni), __fadd2_rn(ft, nf));
-          const float2 y = __fmul2_rn(make_float2(a0, a1), __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), be));
-          a0 = static_cast<unsigned>(s - l) <= w ? y.x : 0.0f;
-          a1 = static_cast<unsigned>(s + 1 - l) <= w ? y.y : 0.0f;
-        };
-        two(r[i], r[i + 1], i0, f0, l0, w0);
-        two(r[i + 2], r[i + 3], i1, f1, l1, w1);
-      };
-      float s0 = 1.0f, s1 = 1.0f;
-      if constexpr (HALF) {
-        float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll 1
-        for (int q = 0; q <= qd; ++q) {
-          float r[8];
-          tm_ld_16x16(tw + kPtColScore + 16 * q, r);
+      for (int e0 = 0; e0 < NH; ++e0) {
+        const float* f = gate_of(g) + e0 * Gate::kHead;
+        const int* first = reinterpret_cast<const int*>(f + Gate::kFirst);
+        const float2 i0 = f2(f[Gate::kInt + t0]), i1 = f2(f[Gate::kInt + t1]);
+        const float2 f0 = f2(f[Gate::kFrac + t0]), f1 = f2(f[Gate::kFrac + t1]);
+        const int l0 = first[t0], l1 = first[t1];
+        const unsigned w0 = t0 - l0, w1 = t1 - l1;
+        // the decayed scores of columns 8j + cc and the next, in place
+        auto decayed = [&](int j, float (&r)[8], int i) {
+          const int s = 8 * j + cc;
+          auto at = [&](int k) { return *reinterpret_cast<const float2*>(f + k + s); };
+          const float2 is = at(Gate::kInt), fs = at(Gate::kFrac), be = at(Gate::kBeta);
+          const float2 ni = make_float2(-is.x, -is.y), nf = make_float2(-fs.x, -fs.y);
+          auto two = [&](float& a0, float& a1, float2 it, float2 ft, int l, unsigned w) {
+            const float2 d = __fadd2_rn(__fadd2_rn(it, ni), __fadd2_rn(ft, nf));
+            const float2 y = __fmul2_rn(make_float2(a0, a1), __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), be));
+            a0 = static_cast<unsigned>(s - l) <= w ? y.x : 0.0f;
+            a1 = static_cast<unsigned>(s + 1 - l) <= w ? y.y : 0.0f;
+          };
+          two(r[i], r[i + 1], i0, f0, l0, w0);
+          two(r[i + 2], r[i + 3], i1, f1, l1, w1);
+        };
+        // columns right of this warp's diagonal block are never written: zero
+        unsigned char* pb = sm + L::kP + (NH * buf + e0) * L::kPanel + t0 * 128 + 2 * cc;
+        auto put = [&](int j, const float* r) {
+          const int at = (j ^ (t0 & 7)) << 4;  // t1 & 7 is the same
+          *reinterpret_cast<uint32_t*>(pb + at) = E::narrow2(r[0], r[1]);
+          *reinterpret_cast<uint32_t*>(pb + 1024 + at) = E::narrow2(r[2], r[3]);
+        };
+        if constexpr (HALF) {
+          // the whole row at once, for its scale
+          float r[4][8];
+          float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q <= qd) tm_ld_16x16(tw + Col::kScore + 16 * q, r[q]);
           wait_ld();
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            decayed(2 * q + e, r, 4 * e);
-            m0 = fmaxf(m0, fmaxf(fabsf(r[4 * e]), fabsf(r[4 * e + 1])));
-            m1 = fmaxf(m1, fmaxf(fabsf(r[4 * e + 2]), fabsf(r[4 * e + 3])));
-          }
-        }
+          for (int q = 0; q < 4; ++q) {
+            if (q > qd) continue;
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
-          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
-        }
-        float k0, k1;
-        s0 = row_scale(m0, k0);
-        s1 = row_scale(m1, k1);
-        if (lane % 4 == 0) {
-          float* sp = reinterpret_cast<float*>(sm + L::kScaleP) + 64 * (g & 3);
-          sp[t0] = k0;
-          sp[t1] = k1;
-        }
-      }
-      // columns right of this warp's diagonal block are never written: zero
-      unsigned char* pb = sm + L::kP + buf * L::kPanel + t0 * 128 + 2 * cc;
+            for (int e = 0; e < 2; ++e) {
+              decayed(2 * q + e, r[q], 4 * e);
+              m0 = fmaxf(m0, fmaxf(fabsf(r[q][4 * e]), fabsf(r[q][4 * e + 1])));
+              m1 = fmaxf(m1, fmaxf(fabsf(r[q][4 * e + 2]), fabsf(r[q][4 * e + 3])));
+            }
+          }
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+          }
+          float k0, k1;
+          const float s0 = row_scale(m0, k0), s1 = row_scale(m1, k1);
+          if (lane % 4 == 0) {
+            float* sp = reinterpret_cast<float*>(sm + L::kScaleP) + 64 * (NH * (g & 3) + e0);
+            sp[t0] = k0;
+            sp[t1] = k1;
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (q > qd) continue;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float y[4] = {r[q][4 * e] * s0, r[q][4 * e + 1] * s0, r[q][4 * e + 2] * s1, r[q][4 * e + 3] * s1};
+              put(2 * q + e, y);
+            }
+          }
+        } else {
 #pragma unroll 1
-      for (int q = 0; q <= qd; ++q) {
-        float r[8];
-        tm_ld_16x16(tw + kPtColScore + 16 * q, r);
-        wait_ld();
+          for (int q = 0; q <= qd; ++q) {
+            float r[8];
+            tm_ld_16x16(tw + Col::kScore + 16 * q, r);
+            wait_ld();
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = 2 * q + e;
-          decayed(j, r, 4 * e);
-          const int at = (j ^ (t0 & 7)) << 4;  // t1 & 7 is the same
-          if constexpr (HALF) {
-            r[4 * e] *= s0;
-            r[4 * e + 1] *= s0;
-            r[4 * e + 2] *= s1;
-            r[4 * e + 3] *= s1;
+            for (int e = 0; e < 2; ++e) {
+              decayed(2 * q + e, r, 4 * e);
+              put(2 * q + e, r + 4 * e);
+            }
           }
-          *reinterpret_cast<uint32_t*>(pb + at) = E::narrow2(r[4 * e], r[4 * e + 1]);
-          *reinterpret_cast<uint32_t*>(pb + 1024 + at) = E::narrow2(r[4 * e + 2], r[4 * e + 3]);
         }
       }
       fence_before();
@@ -713,24 +808,24 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       signal(B::kPFull + buf);
       if (lane == 0) {
         arrive(bar(B::kScFree));
-        arrive(bar(B::kGateFree + st));
+        arrive(bar(B::kGateFree + g % NG));
       }
     }
   } else if (warp < 12) {
     // ---- outputs
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsO));
     constexpr int WR = MDV / 4;  // rows of a warp
     const int m = lane >> 3;     // the matrix whose row address this lane gives to stmatrix
 #pragma unroll 1
     for (; outputs; ++g) {
       const int st = g % NST;
-      if (!(ok = wait_all(B::kGateFull + st, g / NST)) || chunk_of(g).n < 0) break;
-      const int t = chunk_of(g).t, n = chunk_of(g).n, head = chunk_of(g).head;
-      const int row = chunk_of(g).row + WR * qd;  // the warp's first row
+      if (!(ok = wait_all(B::kGateFull + g % NG, g / NG)) || chunk_of(g).n < 0) break;
+      const int t = chunk_of(g).t, n = chunk_of(g).n, head = chunk_of(g).head + mine;
+      const int row = chunk_of(g).row + hrow;  // the warp's first row
       if (!(ok = wait_all(B::kOFull, g))) break;
       fence_after();
-      const float* eg = gate_of(g) + Gate::kDecay + 2 * (lane % 4);
-      const float* sp = reinterpret_cast<const float*>(sm + L::kScaleP) + 64 * (g & 3) + 2 * (lane % 4);
+      const float* eg = gate_of(g) + mine * Gate::kHead + Gate::kDecay + 2 * (lane % 4);
+      const float* sp = reinterpret_cast<const float*>(sm + L::kScaleP) + 64 * (NH * (g & 3) + mine) + 2 * (lane % 4);
       const float* ss = reinterpret_cast<const float*>(sm + L::kScaleS) + 128 * (g & 1) + WR * qd + lane / 4;
       // W is formed and O2 is done with v: its place holds this warp's
       // outputs [64 tokens][WR rows], swizzled as the store wants
@@ -740,8 +835,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int h = i >> 1, q = i & 1;  // 16 rows, 32 tokens
         const uint32_t from = tw + (static_cast<uint32_t>(16 * h) << 16) + 32 * q;
         float u[16], y[16];
-        tm_ld_16x32(from + kPtColO1, u);
-        tm_ld_16x32(from + kPtColO2, y);
+        tm_ld_16x32(from + Col::kO1, u);
+        tm_ld_16x32(from + Col::kO2 + 64 * mine, y);
         const float sa = HALF ? ss[16 * h] : 1.0f, sb = HALF ? ss[16 * h + 8] : 1.0f;
         float2 d[4];
 #pragma unroll
@@ -774,7 +869,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       fence_before();
       fence_async_smem();
       signal(B::kOFree);
-      if (lane == 0) arrive(bar(B::kGateFree + st));
+      if (lane == 0) arrive(bar(B::kGateFree + g % NG));
       if (n == C) {
         if (lane == 0 && row < p.dv) tma_store3(&mo, out, row, head, t);
       } else {
@@ -801,7 +896,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     }
   } else {
     // ---- the state into tensor memory, W one chunk ahead, the state's update
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsS));
     const int half = (warp - 12) >> 2;  // which half of W's tokens and of S's columns
     constexpr int SC = DK / 2;
     float2 S[SC / 2];
@@ -848,7 +943,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           for (int q = 0; q < 2; ++q)
             ldsm4_t(at + 16 * q * 128, v[h][4 * q], v[h][4 * q + 1], v[h][4 * q + 2], v[h][4 * q + 3]);
         }
-        const float* wt = gate_of(n) + Gate::kW + 32 * half + 2 * (lane % 4);
+        const float* wt = gate_of(n) + mine * Gate::kHead + Gate::kW + 32 * half + 2 * (lane % 4);
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const float2*>(wt + 8 * j);
       }
@@ -895,7 +990,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           u[h][1] = row_scale(worst(n & 3, row + 8), back);
         }
       }
-      const uint32_t at = tw + kPtColW + 64 * (n & 1) + 16 * half;
+      const uint32_t at = tw + Col::kW + 64 * (n % Col::kWBufs) + 16 * half;
 #pragma unroll
       for (int h = 0; h < HS; ++h) {
         uint32_t hi[8], lo[8];
@@ -914,7 +1009,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       }
       wait_st();
       fence_before();
-      signal(B::kWFull + (n & 1));
+      signal(B::kWFull + n % Col::kWBufs);
       return true;
     };
     // the state before chunk g into tensor memory, rounded to E
@@ -942,7 +1037,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           const float2 u = S[16 * q + j];
           r[j] = HALF ? E::narrow2(u.x * up, u.y * up) : E::narrow2(u.x, u.y);
         }
-        tm_st16u(tw + kPtColS + half * (SC / 2) + 16 * q, r);
+        tm_st16u(tw + Col::kS + half * (SC / 2) + 16 * q, r);
       }
       wait_st();
       fence_before();
@@ -952,7 +1047,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     // this thread's part of a head's state, or null where it has none
     auto part = [&](const float* state, int row) {
       row += irow;
-      return irow >= 0 && row < p.dv && state != nullptr ? const_cast<float*>(state) + static_cast<size_t>(row) * DK + SC * half
+      return irow >= 0 && row < rows && state != nullptr ? const_cast<float*>(state) + static_cast<size_t>(row) * DK + SC * half
                                                          : nullptr;
     };
     float decay = 1.0f;  // of the item so far
@@ -976,20 +1071,22 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
       }
       if (outputs && !(ok = put_state())) break;
-      if (!(ok = wait_all(B::kGateFull + (g + 1) % NST, (g + 1) / NST))) break;
+      if (!(ok = wait_all(B::kGateFull + (g + 1) % NG, (g + 1) / NG))) break;
       more = chunk_of(g + 1).n >= 0;
-      if (more && !(ok = form_w(g + 1))) break;
+      // with two buffers W is formed while KV(g) runs, with one behind it
+      if (Col::kWBufs == 2 && more && !(ok = form_w(g + 1))) break;
       if (!(ok = wait_all(B::kKvFull, g))) break;
+      if (Col::kWBufs == 1 && more && !(ok = form_w(g + 1))) break;
       fence_after();
-      const float gamma = chunk_of(g).last;
+      const float gamma = chunk_of(g).last[mine];
       decay *= gamma;
       float back = 1.0f;
       if constexpr (HALF) row_scale(worst(g & 3, max(irow, 0)), back);
 #pragma unroll
       for (int q = 0; q < SC / 32; ++q) {
         float r[2][16];
-        tm_ld16(tw + kPtColKV + SC * half + 32 * q, r[0]);
-        tm_ld16(tw + kPtColKV + SC * half + 32 * q + 16, r[1]);
+        tm_ld16(tw + Col::kKV + SC * half + 32 * q, r[0]);
+        tm_ld16(tw + Col::kKV + SC * half + 32 * q + 16, r[1]);
         wait_ld();
         if (q == SC / 32 - 1) {
           fence_before();
@@ -1016,9 +1113,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             store8<F32>(to + j, v);
           }
         }
-        if (chunk_of(g).decay != nullptr && tid == 384 && chunk_of(g).row == 0) *chunk_of(g).decay = decay;
+        if (chunk_of(g).decay != nullptr && half == 0 && lane == 0 && hrow == 0 && chunk_of(g).row == 0)
+          chunk_of(g).decay[mine] = decay;
       }
-      signal(B::kGateFree + g % NST);
+      signal(B::kGateFree + g % NG);
       if (lane == 0) arrive(bar(B::kEmpty + g % NST));
     }
   }
@@ -1033,6 +1131,49 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   if (warp == 3) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512u) : "memory");
 }
 
+// The units in falling order of their chunks (those of one length in any
+// order: items do not depend on one another), by counting; the tickets of the
+// launches that follow back to 0; and whether a prompt is cut.  One CTA.
+constexpr int kOrderThreads = 1024;
+static __global__ void __launch_bounds__(kOrderThreads) packed_order_kernel(const PackedTcParams a, int units, int* order,
+                                                                            int* tickets) {
+  __shared__ int count[kOrderThreads];  // units of each length, then the place of their first
+  __shared__ int cut;
+  const int tid = threadIdx.x;
+  grid_dep_launch();
+  grid_dep_wait();
+  auto bucket = [&](int u) {  // longest first; very long ones together
+    int seq, seg, begin, end;
+    unit_at(a, u, seq, seg);
+    prompt_bounds(a.p.starts, seq, a.p.tokens, begin, end);
+    int n = end - begin;
+    if (a.seg > 0) {
+      if (n > a.seg) cut = 1;
+      n = seg < 0 ? 0 : min(max(n - seg * a.seg, 0), a.seg);
+    }
+    return kOrderThreads - 1 - min((n + kPtChunk - 1) / kPtChunk, kOrderThreads - 1);
+  };
+  count[tid] = 0;
+  if (tid == 0) cut = 0;
+  if (tid < 2) tickets[tid] = 0;
+  __syncthreads();
+  for (int u = tid; u < units; u += kOrderThreads) atomicAdd(&count[bucket(u)], 1);
+  __syncthreads();
+  const int own = count[tid];
+  int sum = own;
+  for (int d = 1; d < kOrderThreads; d <<= 1) {
+    const int before = tid >= d ? count[tid - d] : 0;
+    __syncthreads();
+    sum += before;
+    count[tid] = sum;
+    __syncthreads();
+  }
+  count[tid] = sum - own;
+  __syncthreads();
+  for (int u = tid; u < units; u += kOrderThreads) order[atomicAdd(&count[bucket(u)], 1)] = u;
+  if (tid == 0) tickets[2] = cut;
+}
+
 // The states that segments left from zero, joined in order: stored state k of
 // a prompt becomes the state after its segment k.  A thread owns four
 // elements of a head's state (`quads` CTAs a state); the segments' loads are
@@ -1041,6 +1182,9 @@ constexpr int kJoinThreads = 128;
 template <int DK>
 __global__ void __launch_bounds__(kJoinThreads) packed_join_kernel(const PackedTcParams a, int quads) {
   const PackedParams& p = a.p;
+  grid_dep_launch();
+  grid_dep_wait();
+  if (a.cut != nullptr && __ldg(a.cut) == 0) return;
   const int seq = blockIdx.x / quads, head = blockIdx.y;
   int begin, end;
   prompt_bounds(p.starts, seq, p.tokens, begin, end);

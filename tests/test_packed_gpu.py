@@ -230,17 +230,42 @@ def test_bounds_are_clamped(dtype):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
-@pytest.mark.parametrize("lens,H,decay", [([5000], 2, (0.9, 1.0)), ([4097, 0, 900], 1, (0.999, 1.0)), ([2500], 3, (1.0, 1.0)),
-                                          ([30000], 1, (0.9999, 1.0))])
-def test_long_prompts(lens, H, decay, dtype):
+@pytest.mark.parametrize("lens,H,decay,dk,dv", [
+    ([5000], 2, (0.9, 1.0), 128, 128), ([4097, 0, 900], 1, (0.999, 1.0), 128, 128), ([2500], 3, (1.0, 1.0), 128, 128),
+    ([30000], 1, (0.9999, 1.0), 128, 128), ([5000, 33], 4, (0.9, 1.0), 128, 64), ([3000, 64, 2000], 6, (0.99, 1.0), 64, 64),
+    ([2000, 700], 3, (0.9, 1.0), 64, 64), ([2100], 5, (0.9, 1.0), 64, 208)])
+def test_long_prompts(lens, H, decay, dk, dv, dtype):
     """Prompts that few heads leave to few CTAs: the long axis is split."""
-    dk, dv = 128, 128
     rng = np.random.default_rng(11)
     starts, q, k, v, alpha, beta, S0 = _make(rng, lens, H, 1, dk, dv, dtype, decay=decay)
     o, S = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
     _compare(o, S, starts, q, k, v, alpha, beta, S0, H, dtype)
     o2, S2 = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
     assert torch.equal(o[:int(starts[-1])], o2[:int(starts[-1])]) and torch.equal(S, S2)  # no order but one
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+@pytest.mark.parametrize("dk,dv,H,Hk", [(64, 64, 4, 2), (128, 128, 2, 2), (64, 96, 2, 1)])
+def test_many_prompts(dk, dv, H, Hk, dtype):
+    """More prompts and heads than SMs: items are taken by ticket, the longest first."""
+    rng = np.random.default_rng(15)
+    lens = [int(x) for x in rng.integers(0, 300, 200)]
+    starts, q, k, v, alpha, beta, S0 = _make(rng, lens, H, Hk, dk, dv, dtype)
+    o, S = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    _compare(o, S, starts, q, k, v, alpha, beta, S0, H // Hk, dtype)
+    o2, S2 = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    end = int(starts[-1])
+    assert torch.equal(o[:end], o2[:end]) and torch.equal(S, S2)
+
+
+@pytest.mark.parametrize("lens", [[12000] + [900] * 31, [1300] * 32], ids=["cut", "whole"])
+def test_long_prompt_among_many(lens):
+    """A batch of many long prompts, in which one is cut into segments, or none is."""
+    dk, dv, H, Hk = 64, 64, 8, 8
+    rng = np.random.default_rng(16)
+    starts, q, k, v, alpha, beta, S0 = _make(rng, lens, H, Hk, dk, dv, BF16, decay=(0.99, 1.0))
+    o, S = _run(starts, q, k, v, alpha, beta, S0, dk, dv)
+    _compare(o, S, starts, q, k, v, alpha, beta, S0, 1, BF16)
 
 
 def test_no_tokens_and_no_prompts():
