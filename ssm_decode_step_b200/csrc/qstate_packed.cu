@@ -199,6 +199,17 @@ cudaError_t launch_packed_tc(const PackedParams& p0, int sequences, void* worksp
   return launch_next(kernel, dim3(grid), kPtThreads, kSmem, stream, mq, mk, mv, mo, a);
 }
 
+// Prompts of a few tokens go through the recurrence: a chunk costs the tensor
+// cores' pipeline 6.8 us with one prompt of 16 heads of 64 x 64 (9.4 us of
+// 128 x 128) whatever its length, a token the recurrence 2.7 us and about
+// 0.25 us more for each one behind it (3.1 and 0.3).  With 64 prompts of
+// 128 x 128 they meet at 4 tokens (48 us).  The lengths are not known here:
+// kFewTokens bounds what one long prompt among short ones can cost.
+constexpr int kShortPrompt = 4, kFewTokens = 512;
+bool short_prompts(int tokens, int sequences) {
+  return tokens <= kFewTokens && tokens <= static_cast<long long>(kShortPrompt) * sequences;
+}
+
 template <class E, int DK>
 cudaError_t launch_tc(const PackedParams& p, int sequences, void* ws, cudaStream_t stream) {
   if (two_heads(p.dv, p.share)) return launch_packed_tc<E, DK, 128, 2>(p, sequences, ws, stream);
@@ -271,7 +282,7 @@ qs_status qstate_prefill_packed(const qs_config* cfg, const qs_tokens* batch, in
   p.dv = c.dv;
   p.blocks = 0;
   cudaError_t e;
-  if (batch->dtype != QS_F32 && any) {
+  if (batch->dtype != QS_F32 && any && !short_prompts(batch->tokens, sequences)) {
 #define QS_TC(E) (c.dk == 64 ? launch_tc<E, 64>(p, sequences, workspace, stream) \
                              : launch_tc<E, 128>(p, sequences, workspace, stream))
     e = batch->dtype == QS_F16 ? QS_TC(F16) : QS_TC(BF16);

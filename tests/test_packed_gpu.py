@@ -90,7 +90,7 @@ def _run(starts, q, k, v, alpha, beta, S0, dk, dv, **kw):
 
 LENGTHS = {
     "one": [1], "two": [2], "chunk-1": [63], "chunk": [64], "chunk+1": [65], "long": [1000],
-    "ragged": [0, 1, 130, 0, 64, 17, 300, 63, 5, 0], "many": [7] * 50, "empty": [0, 0],
+    "ragged": [0, 1, 130, 0, 64, 17, 300, 63, 5, 0], "many": [7] * 50, "empty": [0, 0], "tokens": [1, 2, 0, 4, 1, 3, 9, 1], "single": [1] * 40,
 }
 
 
