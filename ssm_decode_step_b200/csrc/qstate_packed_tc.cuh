@@ -127,10 +127,10 @@ struct PtLayout {
   static constexpr int kPanel = kPtChunk * 128;  // 64 tokens x 64 columns, 128-byte swizzled
   static constexpr int kQ = 0, kK = DK / 64 * kPanel, kV = 2 * kK, kStage = kV + MDV / 64 * kPanel;
   static constexpr int kStages = DK == 128 ? (NH == 2 ? 3 : 4) : NH == 2 ? 4 : 5;
-  static constexpr int kGates = DK == 128 && NH == 1 ? 5 : 8;  // ring of gate slots, longer than the stages'
+  static constexpr int kGates = DK == 128 && NH == 1 ? 4 : 8;  // ring of gate slots
   static constexpr int kP = kStages * kStage;           // two buffers of 64 x 64 a head
   static constexpr int kGate = kP + 2 * NH * kPanel;         // see Gate
-  static constexpr int kGateSlot = NH * 6 * 256 + 128;
+  static constexpr int kGateSlot = NH * 7 * 256 + 128;
   static constexpr int kScaleS = kGate + kGates * kGateSlot;  // fp16: 2 x 128 row scales of S
   static constexpr int kScaleP = kScaleS + 1024;               // fp16: 4 x 64 row scales of P a head
   static constexpr int kMax = kScaleP + 1024 * NH;                  // fp16: 6 x 2 x 128 row maxima, 4 of W and 2 of S
@@ -140,11 +140,12 @@ struct PtLayout {
 };
 
 // A chunk's factors, in floats from its gate slot, for each head kHead apart:
-// the integers and fractions of G, beta, W's weights 2^{G_C - G} beta, 2^G and
-// the first token that a token still sees (int).  Behind the last head's, what
-// the chunk is (Chunk).
+// the integers and fractions of G, beta, W's weights 2^{G_C - G} beta, 2^G, the
+// first token that a token still sees (int), and 2^{G_e - G} beta with e the
+// last token of its block of 16.  Behind the last head's, what the chunk is
+// (Chunk).
 struct Gate {
-  static constexpr int kInt = 0, kFrac = 64, kBeta = 128, kW = 192, kDecay = 256, kFirst = 320, kHead = 384;
+  static constexpr int kInt = 0, kFrac = 64, kBeta = 128, kW = 192, kDecay = 256, kFirst = 320, kCol = 384, kHead = 448;
 };
 struct Chunk {
   const float* from;  // first chunk of an item: the head's state before it (null: zeros)
@@ -197,30 +198,21 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// One look at the phase of the given parity.
-__device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {
+// Wait for the phase of the given parity; false where it does not complete in
+// kPtPolls looks.  The loop is written out so that it stays this short: a role
+// waits some five times a chunk, and what a wait costs beyond the event counts.
+constexpr uint32_t kPtPolls = 1u << 18;
+__device__ __forceinline__ bool mbar_wait_or_fail(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n\t"
+      "WAIT:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+      "add.u32 n, n, 1;\n\tsetp.lt.u32 p, n, %3;\n\t@p bra WAIT;\n\tsetp.ne.u32 p, n, n;\n\t"
+      "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(done)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "n"(kPtPolls)
       : "memory");
   return done != 0;
-}
-
-// Wait for that phase; false once this wait, or another of the CTA's
-// (`failed`), gave up.
-constexpr uint32_t kPtPolls = 1u << 18;
-__device__ __forceinline__ bool mbar_wait_or_fail(uint32_t bar, uint32_t parity, volatile uint32_t* failed) {
-  uint32_t polls = 0;
-#pragma unroll 1
-  while (!mbar_done(bar, parity)) {
-    if ((++polls & 1023u) == 0 && (polls >= kPtPolls || *failed)) {
-      *failed = 1;
-      return false;
-    }
-  }
-  return true;
 }
 
 __device__ __forceinline__ void mma16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
@@ -406,10 +398,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   const uint32_t tw = tm + (static_cast<uint32_t>(32 * qd) << 16);  // this warp's lanes
 
   // Completion number n of a barrier (n < 0 is complete from the start);
-  // `wait` for one thread, `wait_all` for a whole warp.  False once this wait
-  // or another gave up.
+  // `wait` for one thread, `wait_all` for a whole warp.  False where it gave up.
   auto wait = [&](int b, int n) -> bool {
-    return mbar_wait_or_fail(bar(b), static_cast<uint32_t>(n) & 1u, failed);
+    return mbar_wait_or_fail(bar(b), static_cast<uint32_t>(n) & 1u);
   };
   auto wait_all = [&](int b, int n) -> bool { return __all_sync(0xffffffffu, wait(b, n)); };
   // The warp's work so far is visible to whoever waits for this arrival.
@@ -700,6 +691,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             f[Gate::kW + t] = t >= rc[e] ? be * ex2(real(gc[e] - x)) : 0.0f;
             f[Gate::kDecay + t] = r < 0 ? exp2f(real(x)) : 0.0f;
             first[t] = max(r, 0);
+            // to the end of its block; a reset on the way forgets it
+            const long long xe = __shfl_sync(0xffffffffu, x, lane | 15);
+            const int re = __shfl_sync(0xffffffffu, r, lane | 15);
+            f[Gate::kCol + t] = t >= re ? be * ex2(real(xe - x)) : 0.0f;
           };
           put(lane, x0[e], now.b0[e], r0[e]);
           put(lane + 32, x1[e], now.b1[e], r1[e]);
@@ -731,46 +726,62 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       for (int e0 = 0; e0 < NH; ++e0) {
         const float* f = gate_of(g) + e0 * Gate::kHead;
         const int* first = reinterpret_cast<const int*>(f + Gate::kFirst);
-        const float2 i0 = f2(f[Gate::kInt + t0]), i1 = f2(f[Gate::kInt + t1]);
-        const float2 f0 = f2(f[Gate::kFrac + t0]), f1 = f2(f[Gate::kFrac + t1]);
+        const float i0 = f[Gate::kInt + t0], i1 = f[Gate::kInt + t1], f0 = f[Gate::kFrac + t0], f1 = f[Gate::kFrac + t1];
         const int l0 = first[t0], l1 = first[t1];
-        const unsigned w0 = t0 - l0, w1 = t1 - l1;
-        // the decayed scores of columns 8j + cc and the next, in place
-        auto decayed = [&](int j, float (&r)[8], int i) {
-          const int s = 8 * j + cc;
+        // the scores of this warp's rows: r[0] the block on the diagonal, r[1 + q]
+        // column block q left of it; element pairs 8e + cc of row t0, then of t1
+        float r[4][8];
+        tm_ld_16x16(tw + Col::kScore + 16 * qd, r[0]);
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          if (q < qd) tm_ld_16x16(tw + Col::kScore + 16 * q, r[1 + q]);
+        wait_ld();
+        if (e0 == NH - 1) {
+          fence_before();
+          signal(B::kScFree);
+        }
+        // on the diagonal: every element's own decay
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int s = 16 * qd + 8 * e + cc;
           auto at = [&](int k) { return *reinterpret_cast<const float2*>(f + k + s); };
           const float2 is = at(Gate::kInt), fs = at(Gate::kFrac), be = at(Gate::kBeta);
           const float2 ni = make_float2(-is.x, -is.y), nf = make_float2(-fs.x, -fs.y);
-          auto two = [&](float& a0, float& a1, float2 it, float2 ft, int l, unsigned w) {
-            const float2 d = __fadd2_rn(__fadd2_rn(it, ni), __fadd2_rn(ft, nf));
+          auto two = [&](float& a0, float& a1, float it, float ft, int l, int t) {
+            const float2 d = __fadd2_rn(__fadd2_rn(f2(it), ni), __fadd2_rn(f2(ft), nf));
             const float2 y = __fmul2_rn(make_float2(a0, a1), __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), be));
-            a0 = static_cast<unsigned>(s - l) <= w ? y.x : 0.0f;
-            a1 = static_cast<unsigned>(s + 1 - l) <= w ? y.y : 0.0f;
+            a0 = static_cast<unsigned>(s - l) <= static_cast<unsigned>(t - l) ? y.x : 0.0f;
+            a1 = static_cast<unsigned>(s + 1 - l) <= static_cast<unsigned>(t - l) ? y.y : 0.0f;
           };
-          two(r[i], r[i + 1], i0, f0, l0, w0);
-          two(r[i + 2], r[i + 3], i1, f1, l1, w1);
-        };
-        // columns right of this warp's diagonal block are never written: zero
-        unsigned char* pb = sm + L::kP + (NH * buf + e0) * L::kPanel + t0 * 128 + 2 * cc;
-        auto put = [&](int j, const float* r) {
-          const int at = (j ^ (t0 & 7)) << 4;  // t1 & 7 is the same
-          *reinterpret_cast<uint32_t*>(pb + at) = E::narrow2(r[0], r[1]);
-          *reinterpret_cast<uint32_t*>(pb + 1024 + at) = E::narrow2(r[2], r[3]);
-        };
-        if constexpr (HALF) {
-          // the whole row at once, for its scale
-          float r[4][8];
-          float m0 = 0.0f, m1 = 0.0f;
+          two(r[0][4 * e], r[0][4 * e + 1], i0, f0, l0, t0);
+          two(r[0][4 * e + 2], r[0][4 * e + 3], i1, f1, l1, t1);
+        }
+        // left of it: 2^{G_t - G_e} 2^{G_e - G_s} beta_s with e the column block's
+        // last token; both exponents are at most 0
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (q <= qd) tm_ld_16x16(tw + Col::kScore + 16 * q, r[q]);
-          wait_ld();
+        for (int q = 0; q < 3; ++q) {
+          if (q >= qd) continue;
+          const int end = 16 * q + 15;
+          const float ie = f[Gate::kInt + end], fe = f[Gate::kFrac + end];
+          const float2 a0 = f2(l0 <= end ? ex2((i0 - ie) + (f0 - fe)) : 0.0f);
+          const float2 a1 = f2(l1 <= end ? ex2((i1 - ie) + (f1 - fe)) : 0.0f);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 col = *reinterpret_cast<const float2*>(f + Gate::kCol + 16 * q + 8 * e + cc);
+            float* x = r[1 + q] + 4 * e;
+            const float2 y0 = __fmul2_rn(__fmul2_rn(make_float2(x[0], x[1]), col), a0);
+            const float2 y1 = __fmul2_rn(__fmul2_rn(make_float2(x[2], x[3]), col), a1);
+            x[0] = y0.x, x[1] = y0.y, x[2] = y1.x, x[3] = y1.y;
+          }
+        }
+        float s0 = 1.0f, s1 = 1.0f;
+        if constexpr (HALF) {
+          float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             if (q > qd) continue;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              decayed(2 * q + e, r[q], 4 * e);
               m0 = fmaxf(m0, fmaxf(fabsf(r[q][4 * e]), fabsf(r[q][4 * e + 1])));
               m1 = fmaxf(m1, fmaxf(fabsf(r[q][4 * e + 2]), fabsf(r[q][4 * e + 3])));
             }
@@ -781,42 +792,32 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
           }
           float k0, k1;
-          const float s0 = row_scale(m0, k0), s1 = row_scale(m1, k1);
+          s0 = row_scale(m0, k0);
+          s1 = row_scale(m1, k1);
           if (lane % 4 == 0) {
             float* sp = reinterpret_cast<float*>(sm + L::kScaleP) + 64 * (NH * (g & 3) + e0);
             sp[t0] = k0;
             sp[t1] = k1;
           }
+        }
+        // columns right of the diagonal block are never written: zero
+        unsigned char* pb = sm + L::kP + (NH * buf + e0) * L::kPanel + t0 * 128 + 2 * cc;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (q > qd) continue;
+        for (int q = 0; q < 4; ++q) {
+          if (q > qd) continue;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float y[4] = {r[q][4 * e] * s0, r[q][4 * e + 1] * s0, r[q][4 * e + 2] * s1, r[q][4 * e + 3] * s1};
-              put(2 * q + e, y);
-            }
-          }
-        } else {
-#pragma unroll 1
-          for (int q = 0; q <= qd; ++q) {
-            float r[8];
-            tm_ld_16x16(tw + Col::kScore + 16 * q, r);
-            wait_ld();
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              decayed(2 * q + e, r, 4 * e);
-              put(2 * q + e, r + 4 * e);
-            }
+          for (int e = 0; e < 2; ++e) {
+            const int at = ((2 * (q == 0 ? qd : q - 1) + e) ^ (t0 & 7)) << 4;  // t1 & 7 is the same
+            const float* x = r[q] + 4 * e;
+            *reinterpret_cast<uint32_t*>(pb + at) = HALF ? E::narrow2(x[0] * s0, x[1] * s0) : E::narrow2(x[0], x[1]);
+            *reinterpret_cast<uint32_t*>(pb + 1024 + at) = HALF ? E::narrow2(x[2] * s1, x[3] * s1) : E::narrow2(x[2], x[3]);
           }
         }
       }
       fence_before();
       fence_async_smem();
       signal(B::kPFull + buf);
-      if (lane == 0) {
-        arrive(bar(B::kScFree));
-        arrive(bar(B::kGateFree + g % NG));
-      }
+      if (lane == 0) arrive(bar(B::kGateFree + g % NG));
     }
   } else if (warp < 12) {
     // ---- outputs
