@@ -420,8 +420,8 @@ typedef enum { QS_F32 = 0, QS_F16 = 1, QS_BF16 = 2 } qs_dtype;
  *   q, k [tokens][qk_heads][Dk];  v, o [tokens][heads][Dv]   (dtype)
  * Value head h uses q/k head h / (heads / qk_heads).  q, k, v and o are
  * 16-byte aligned and so is every stride (in bytes); strides are at least
- * one token's heads long, so q, k and v may be slices of one buffer; o
- * overlaps none of them. */
+ * one token's heads long, so q, k and v may be slices of one buffer; o's
+ * range, the gaps between its tokens included, overlaps none of theirs. */
 typedef struct {
   int32_t tokens;   /* entries of the batch, or rows of the packed prompts */
   int32_t heads;    /* value heads: tiles of a slot                        */

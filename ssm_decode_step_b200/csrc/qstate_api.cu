@@ -114,7 +114,7 @@ int lrb_rpad(int rank) { return (rank + 3) / 4 * 4; }
 
 extern "C" {
 
-int qstate_version(void) { return 100; }
+int qstate_version(void) { return 200; }
 
 qs_status qstate_selfcheck(unsigned long long* mismatches, cudaStream_t stream) {
   if (mismatches == nullptr || !aligned(mismatches, 8)) return QS_ERR_INVALID_ARG;

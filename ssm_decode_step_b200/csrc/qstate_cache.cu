@@ -113,7 +113,6 @@ qs_status qstate_cache_step(const qs_config* cfg, const qs_tokens* batch, const 
   st = check_pool(cfg, batch->heads);
   if (st != QS_OK) return st;
   if (cfg->policy == QS_SCALE_YOKED) return QS_ERR_UNSUPPORTED;
-  if (!batch_fits(cfg, batch->tokens, batch->heads)) return QS_ERR_UNSUPPORTED;
   if (batch->tokens == 0 || cfg->num_tiles == 0) return QS_OK;
   const bool diag = cfg->decay == QS_DECAY_DIAGONAL;
   if (!slots || !codes || !scales || !k || !v || !alpha || !beta || (o && !q)) return QS_ERR_INVALID_ARG;
@@ -123,6 +122,7 @@ qs_status qstate_cache_step(const qs_config* cfg, const qs_tokens* batch, const 
   TokenRanges t;
   st = check_tokens(cfg, batch, q, k, v, o, &t);
   if (st != QS_OK) return st;
+  if (!batch_fits(cfg, batch->tokens, batch->heads)) return QS_ERR_UNSUPPORTED;
   const Sizes z = sizes_of(cfg);
   const size_t tiles = static_cast<size_t>(batch->tokens) * batch->heads;
   const Range w[3] = {range_of(codes, z.codes), range_of(scales, z.scales), t.o};

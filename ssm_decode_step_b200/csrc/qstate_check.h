@@ -97,7 +97,9 @@ inline qs_status check_tokens(const qs_config* c, const qs_tokens* b, const void
   for (int i = 0; i < 4; ++i) {
     out[i] = range_of(nullptr, 0);
     if (ptr[i] == nullptr) continue;
-    if (strides[i] < static_cast<int64_t>(width[i]) || strides[i] > (1LL << 40)) return QS_ERR_INVALID_ARG;
+    // a token's stride fits a tensor map's 40 bits of bytes, and the whole batch 62
+    if (strides[i] < static_cast<int64_t>(width[i]) || strides[i] > (1LL << 37)) return QS_ERR_INVALID_ARG;
+    if (strides[i] > (1LL << 60) / b->tokens) return QS_ERR_INVALID_ARG;
     if ((static_cast<size_t>(strides[i]) * e) % 16 != 0 || !aligned(ptr[i], 16)) return QS_ERR_INVALID_ARG;
     out[i] = range_of(ptr[i], (static_cast<size_t>(b->tokens - 1) * strides[i] + width[i]) * e);
   }

@@ -1,6 +1,6 @@
 // C entry points of the packed prefill (include/qstate.h): argument checks,
 // choice of the kernel, and its launch.  No memory is allocated.
-#include <mutex>
+#include <atomic>
 
 #include "qstate_check.h"
 #include "qstate_launch_impl.cuh"
@@ -144,18 +144,23 @@ template <class E, int DK, int MDV, int NH>
 cudaError_t launch_packed_tc(const PackedParams& p0, int sequences, void* workspace, cudaStream_t stream) {
   auto kernel = packed_tc_kernel<E, DK, MDV, NH>;
   constexpr int kSmem = PtLayout<DK, MDV, NH>::kBytes;
-  static std::once_flag flag;
-  cudaError_t err = cudaSuccess;
-  std::call_once(flag, [&] {
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  });
+  static std::atomic<bool> allowed[64];  // per device
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
+  if (dev >= 64 || !allowed[dev].load(std::memory_order_relaxed)) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (err != cudaSuccess) return err;
+    if (dev < 64) allowed[dev].store(true, std::memory_order_relaxed);
+  }
   PackedTcParams a;
   a.p = p0;
   a.p.blocks = NH == 2 ? 1 : (p0.dv + MDV - 1) / MDV;
   a.sequences = sequences;
   a.seg = segment_tokens(p0.dv, p0.heads, p0.share, p0.tokens, sequences);
   a.local = false;
+  const int quads = (p0.dv * DK / 4 + kJoinThreads - 1) / kJoinThreads;  // CTAs that join a head's state
+  if (static_cast<long long>(quads) * sequences > 0x7fffffffLL) a.seg = 0;
   const long long segs = a.seg > 0 ? p0.tokens / a.seg : 0, units = sequences + segs;
   a.items = static_cast<int>(units * (p0.heads / NH) * a.p.blocks);  // < 2^31: batch_fits, and few segments
   // laid out for the most segments that the batch's sizes allow, as its bytes were
@@ -191,7 +196,6 @@ cudaError_t launch_packed_tc(const PackedParams& p0, int sequences, void* worksp
     first.ticket = a.ticket + 1;
     err = launch_next(kernel, dim3(grid), kPtThreads, kSmem, stream, mq, mk, mv, mo, first);
     if (err != cudaSuccess) return err;
-    const int quads = (p0.dv * DK / 4 + kJoinThreads - 1) / kJoinThreads;
     err = launch_next(packed_join_kernel<DK>, dim3(static_cast<unsigned>(quads) * sequences, p0.heads), kJoinThreads, 0, stream,
                       a, quads);
     if (err != cudaSuccess) return err;

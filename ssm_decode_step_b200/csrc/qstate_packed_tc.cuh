@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         // the running sum of log2(alpha), in units of 2^-32
         auto fixed = [](float v) { return __float2ll_rn(v * 0x1p32f); };
         auto real = [](long long v) { return __ll2float_rn(v) * 0x1p-32f; };
-        float last[NH], bad[NH];
+        float last[NH], bad0[NH], bad1[NH];
         long long x0[NH], x1[NH], gc[NH];
         int r0[NH], r1[NH], rc[NH];
 #pragma unroll
@@ -659,9 +659,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           const int r31 = m0 ? 31 - __clz(m0) : -1;
           r1[e] = (m1 & le) ? 63 - __clz(m1 & le) : r31;
           rc[e] = m1 ? 63 - __clz(m1) : r31;
-          // NaN and infinite decays (which the fixed point cannot hold) spoil
-          // their prompt from here on, as they should
-          bad[e] = __any_sync(0xffffffffu, !(now.a0[e] < INFINITY && now.a1[e] < INFINITY)) ? NAN : 0.0f;
+          // NaN and infinite decays, which the fixed point cannot hold, spoil
+          // their prompt from their token on
+          const uint32_t n0 = __ballot_sync(0xffffffffu, !(now.a0[e] < INFINITY));
+          const uint32_t n1 = __ballot_sync(0xffffffffu, !(now.a1[e] < INFINITY));
+          bad0[e] = (n0 & le) ? NAN : 0.0f;
+          bad1[e] = n0 || (n1 & le) ? NAN : 0.0f;
         }
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -684,21 +687,21 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         for (int e = 0; e < NH; ++e) {
           float* f = gate_of(g) + e * Gate::kHead;
           int* first = reinterpret_cast<int*>(f + Gate::kFirst);
-          auto put = [&](int t, long long x, float be, int r) {
+          auto put = [&](int t, long long x, float be, int r, float bad) {
             f[Gate::kInt + t] = static_cast<float>(static_cast<int>(x >> 32));
-            f[Gate::kFrac + t] = __uint2float_rn(static_cast<uint32_t>(x)) * 0x1p-32f + bad[e];
+            f[Gate::kFrac + t] = __uint2float_rn(static_cast<uint32_t>(x)) * 0x1p-32f + bad;
             f[Gate::kBeta + t] = be;
             f[Gate::kW + t] = t >= rc[e] ? be * ex2(real(gc[e] - x)) : 0.0f;
-            f[Gate::kDecay + t] = r < 0 ? exp2f(real(x)) : 0.0f;
+            f[Gate::kDecay + t] = (r < 0 ? exp2f(real(x)) : 0.0f) + bad;
             first[t] = max(r, 0);
             // to the end of its block; a reset on the way forgets it
             const long long xe = __shfl_sync(0xffffffffu, x, lane | 15);
             const int re = __shfl_sync(0xffffffffu, r, lane | 15);
             f[Gate::kCol + t] = t >= re ? be * ex2(real(xe - x)) : 0.0f;
           };
-          put(lane, x0[e], now.b0[e], r0[e]);
-          put(lane + 32, x1[e], now.b1[e], r1[e]);
-          last[e] = (rc[e] < 0 ? exp2f(real(gc[e])) : 0.0f) + bad[e];
+          put(lane, x0[e], now.b0[e], r0[e], bad0[e]);
+          put(lane + 32, x1[e], now.b1[e], r1[e], bad1[e]);
+          last[e] = (rc[e] < 0 ? exp2f(real(gc[e])) : 0.0f) + __shfl_sync(0xffffffffu, bad1[e], 31);
         }
         __syncwarp();
         const int n = seen[g % (kAhead + 1)].n;

@@ -404,6 +404,8 @@ class _OnDevice:
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.device = dev
+        self._kept = ()       # tensors that the object itself keeps between calls
+        self._seen = set()    # streams that have used them
 
     def _launch(self, what, fn, args, stream):
         import torch
@@ -411,6 +413,11 @@ class _OnDevice:
             handle = _current_stream(self.device.index)
         else:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
+        if handle not in self._seen and not torch.cuda.is_current_stream_capturing():
+            # their memory is not reused before this stream is done with it
+            self._seen.add(handle)
+            for t in self._kept:
+                t.record_stream(torch.cuda.ExternalStream(handle, self.device))
         if torch.cuda.current_device() == self.device.index:
             status = fn(*args, handle)
         else:
@@ -458,6 +465,7 @@ class StateCache(_OnDevice):
         _check_tensor("codes", codes, shapes[0], torch.uint8, self.device)
         _check_tensor("scales", scales, shapes[1], torch.float32, self.device)
         self.codes, self.scales = codes, scales
+        self._kept = (codes, scales)
         self._cc = cfg.c()
         self._ccp = ctypes.byref(self._cc)
 
@@ -551,6 +559,7 @@ class PackedPrefill(_OnDevice):
         self._ccp = ctypes.byref(self._cc)
         need = packed_workspace(cfg, max_tokens, heads, self.qk_heads, max_sequences)
         self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        self._kept = (self.workspace,)
 
     def run(self, starts, q, k, v, alpha, beta, S0=None, S=None, o=None, stream=None):
         """(o, S) of the prompts starts[i]..starts[i+1]-1 (int32 [sequences + 1]) of q, k

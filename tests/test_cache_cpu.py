@@ -67,7 +67,7 @@ def _step(cfg=None, batch=None, **ptrs):
 @pytest.mark.parametrize("bad", [
     dict(tokens=-1), dict(heads=0), dict(heads=5), dict(qk_heads=0), dict(qk_heads=3), dict(dtype=3),
     dict(q_stride=255), dict(k_stride=248), dict(v_stride=250), dict(o_stride=-256), dict(k_stride=260),
-    dict(v_stride=1 << 41),
+    dict(v_stride=1 << 41), dict(tokens=1 << 30, v_stride=1 << 36),
 ])
 def test_step_batch_refusals(bad):
     assert _step(batch=_batch(**bad)) == Q.QS_ERR_INVALID_ARG
