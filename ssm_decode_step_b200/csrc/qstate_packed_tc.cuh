@@ -644,9 +644,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         // the running sum of log2(alpha), in units of 2^-32
         auto fixed = [](float v) { return __float2ll_rn(v * 0x1p32f); };
         auto real = [](long long v) { return __ll2float_rn(v) * 0x1p-32f; };
-        float last[NH], bad0[NH], bad1[NH];
+        float last[NH];
         long long x0[NH], x1[NH], gc[NH];
-        int r0[NH], r1[NH], rc[NH];
+        int r0[NH], r1[NH], rc[NH], bad[NH];
 #pragma unroll
         for (int e = 0; e < NH; ++e) {
           const bool z0 = now.a0[e] < kPtReset, z1 = now.a1[e] < kPtReset;
@@ -663,8 +663,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           // their prompt from their token on
           const uint32_t n0 = __ballot_sync(0xffffffffu, !(now.a0[e] < INFINITY));
           const uint32_t n1 = __ballot_sync(0xffffffffu, !(now.a1[e] < INFINITY));
-          bad0[e] = (n0 & le) ? NAN : 0.0f;
-          bad1[e] = n0 || (n1 & le) ? NAN : 0.0f;
+          bad[e] = n0 ? __ffs(n0) - 1 : n1 ? 31 + __ffs(n1) : C;
         }
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -687,21 +686,22 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         for (int e = 0; e < NH; ++e) {
           float* f = gate_of(g) + e * Gate::kHead;
           int* first = reinterpret_cast<int*>(f + Gate::kFirst);
-          auto put = [&](int t, long long x, float be, int r, float bad) {
+          auto put = [&](int t, long long x, float be, int r) {
+            const float spoilt = t >= bad[e] ? NAN : 0.0f;
             f[Gate::kInt + t] = static_cast<float>(static_cast<int>(x >> 32));
-            f[Gate::kFrac + t] = __uint2float_rn(static_cast<uint32_t>(x)) * 0x1p-32f + bad;
+            f[Gate::kFrac + t] = __uint2float_rn(static_cast<uint32_t>(x)) * 0x1p-32f + spoilt;
             f[Gate::kBeta + t] = be;
             f[Gate::kW + t] = t >= rc[e] ? be * ex2(real(gc[e] - x)) : 0.0f;
-            f[Gate::kDecay + t] = (r < 0 ? exp2f(real(x)) : 0.0f) + bad;
+            f[Gate::kDecay + t] = (r < 0 ? exp2f(real(x)) : 0.0f) + spoilt;
             first[t] = max(r, 0);
             // to the end of its block; a reset on the way forgets it
             const long long xe = __shfl_sync(0xffffffffu, x, lane | 15);
             const int re = __shfl_sync(0xffffffffu, r, lane | 15);
             f[Gate::kCol + t] = t >= re ? be * ex2(real(xe - x)) : 0.0f;
           };
-          put(lane, x0[e], now.b0[e], r0[e], bad0[e]);
-          put(lane + 32, x1[e], now.b1[e], r1[e], bad1[e]);
-          last[e] = (rc[e] < 0 ? exp2f(real(gc[e])) : 0.0f) + __shfl_sync(0xffffffffu, bad1[e], 31);
+          put(lane, x0[e], now.b0[e], r0[e]);
+          put(lane + 32, x1[e], now.b1[e], r1[e]);
+          last[e] = (rc[e] < 0 ? exp2f(real(gc[e])) : 0.0f) + (bad[e] < C ? NAN : 0.0f);
         }
         __syncwarp();
         const int n = seen[g % (kAhead + 1)].n;
