@@ -50,9 +50,9 @@
 // for all, and loops of 16 to 32 columns a turn.  At an item's ends the
 // state's rows pass through the load/store unit (some 4000 cycles of 128 x
 // 128).  Measured on a B200: one prompt of 16384 tokens, 16 heads of 128 x
-// 128, bf16, 116 us (floor of its bytes 42 us); 64 prompts of 256 tokens 98 us
+// 128, bf16, 115 us (floor of its bytes 42 us); 64 prompts of 256 tokens 90 us
 // (62); 32 ragged fp16 prompts, 12000 tokens, 64 heads of 64 x 128 on 8 q/k
-// heads, 296 us (59).
+// heads, 288 us (59).
 #pragma once
 
 #include <cuda.h>
@@ -136,7 +136,9 @@ struct PtLayout {
   static constexpr int kMax = kScaleP + 1024 * NH;                  // fp16: 6 x 2 x 128 row maxima, 4 of W and 2 of S
   static constexpr int kSeen = kMax + 6144;                    // chunks whose gates are being loaded
   static constexpr int kBars = kSeen + 256;
-  static constexpr int kBytes = kBars + 512 + 1024;
+  static constexpr int kItems = kBars + 512;                   // items under way, 4 x 64 bytes
+  static constexpr int kBytes = kItems + 256 + 1024;
+  static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
 // A chunk's factors, in floats from its gate slot, for each head kHead apart:
@@ -341,7 +343,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   unsigned char* const sm = raw + (base - saddr(raw));
   uint32_t* const tslot = reinterpret_cast<uint32_t*>(sm + L::kBars + 8 * B::kCount);
   volatile uint32_t* const failed = tslot + 1;
-  volatile int* const queue = reinterpret_cast<volatile int*>(tslot + 2);  // items under way
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int qd = warp & 3;
   const bool outputs = p.o != nullptr;
@@ -474,16 +475,34 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     if (warp == 0) {
       // ---- loads
       if (lane == 0) {
-        int k = 0;  // items so far
-#pragma unroll 1
-        for (int it = blockIdx.x;; ++k) {
-          // the item to the warp that describes its chunks; items: no more
-          if (!(ok = wait(B::kItemFree + k % 4, k / 4 - 1))) break;
-          queue[k % 4] = it;
+        int k = 0;  // items announced
+        auto announce = [&](const Item& x) -> bool {
+          if (!wait(B::kItemFree + k % 4, k / 4 - 1)) return false;
+          *reinterpret_cast<Item*>(sm + L::kItems + 64 * (k % 4)) = x;
           arrive(bar(B::kItemFull + k % 4));
-          if (it >= items) break;
-          const Item x = item_at(it);
-          it = a.order == nullptr ? items : static_cast<int>(gridDim.x) + atomicAdd(a.ticket, 1);
+          ++k;
+          return true;
+        };
+        // the next item with work (chunks = 0: no more) to the warp that
+        // describes its chunks
+        int it = blockIdx.x;
+        auto find = [&]() {
+          Item x;
+          x.chunks = 0;
+#pragma unroll 1
+          while (it < items) {
+            x = item_at(it);
+            it = a.order == nullptr ? items : -1;
+            if (x.chunks > 0) break;
+            if (it < 0) it = static_cast<int>(gridDim.x) + atomicAdd(a.ticket, 1);
+          }
+          ok = announce(x);
+          return x;
+        };
+        Item x = find();
+#pragma unroll 1
+        while (ok && x.chunks > 0) {
+          Item next{};
 #pragma unroll 1
           for (int c = 0; c < x.chunks; ++c, ++g) {
             const int st = g % NST;
@@ -499,8 +518,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
             for (int i = 0; i < MDV / 64; ++i)
               tma_load3(s + L::kV + i * L::kPanel, &mv, NH == 2 ? 0 : x.blk * MDV + 64 * i, NH == 2 ? x.head + i : x.head, t, f);
+            // The next item is found behind this one's first loads: what it
+            // is, its gates and its state take several trips to memory.
+            if (c == 0) {
+              if (it < 0) it = static_cast<int>(gridDim.x) + atomicAdd(a.ticket, 1);
+              next = find();
+              if (!ok) {
+                ++g;
+                break;
+              }
+            }
           }
-          if (!ok) break;
+          x = next;
         }
         // after a timeout: the copies in flight land before the CTA leaves
         if (!ok)
@@ -579,6 +608,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       // loads are issued kAhead chunks ahead (a token's gates of one head are
       // alone in their sector, so they take a full trip to memory)
       constexpr int kAhead = 2;
+      // chunk g is described once chunk g + kAhead is announced, which waits
+      // until chunk g + kAhead - NST - 1 is done
+      static_assert(kAhead <= NST, "a chunk must not wait for itself");
       struct Gates {
         float a0[NH], a1[NH], b0[NH], b1[NH];
       };
@@ -594,20 +626,20 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         k.n = -1;
         if (c == x.chunks) {
           c = 0;
-#pragma unroll 1
-          for (x.chunks = 0; !done && x.chunks == 0; ++taken) {
+          x.chunks = 0;
+          if (!done) {
             done = !wait_all(B::kItemFull + taken % 4, taken / 4);
-            const int it = queue[taken % 4];
+            if (!done) x = *reinterpret_cast<const Item*>(sm + L::kItems + 64 * (taken % 4));
             signal(B::kItemFree + taken % 4);
-            done = done || it >= items;
-            if (!done) x = item_at(it);
-          }
-          if (x.chunks > 0 && x.from != nullptr) {
-            // the item's state toward L2, a few chunks before it is read
-            const char* from = reinterpret_cast<const char*>(x.from + static_cast<size_t>(x.blk) * MDV * DK);
-            const int bytes = min(MDV, rows - x.blk * MDV) * DK * 4;
+            ++taken;
+            done = done || x.chunks == 0;
+            if (x.chunks > 0 && x.from != nullptr) {
+              // the item's state toward L2, a few chunks before it is read
+              const char* from = reinterpret_cast<const char*>(x.from + static_cast<size_t>(x.blk) * MDV * DK);
+              const int bytes = min(MDV, rows - x.blk * MDV) * DK * 4;
 #pragma unroll 1
-            for (int i = 128 * lane; i < bytes; i += 128 * 32) prefetch_l2(from + i);
+              for (int i = 128 * lane; i < bytes; i += 128 * 32) prefetch_l2(from + i);
+            }
           }
         }
         if (x.chunks > 0) {
