@@ -475,9 +475,11 @@ QS_API qs_status qstate_cache_step(const qs_config* cfg, const qs_tokens* batch,
  * accumulators; the state is carried in FP32 and formed from the
  * activations to about 2^-16 of the magnitudes summed; the operands of the
  * outputs (the decayed scores, and the state where it is read) are rounded
- * to dtype once.  FP32 activations run on the CUDA cores in FP32.
- * A decay of 0 forgets everything before its token; with 16-bit activations
- * a decay below 2^-120 counts as 0.
+ * to dtype once.  FP32 activations, and batches of a few tokens (at most 512,
+ * and at most 4 for each prompt on average), run on the CUDA cores in FP32.
+ * A decay of 0 forgets everything before its token; on the tensor cores a
+ * decay below 2^-120 counts as 0.  A decay that is not finite spoils its
+ * prompt's head from its token on, and nothing else.
  *
  * workspace: device memory of at least qstate_prefill_packed_workspace bytes
  * (which depends on the batch's sizes alone, and grows with tokens and

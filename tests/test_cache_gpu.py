@@ -292,6 +292,24 @@ def test_captured_step_follows_its_slots_and_streams():
     assert torch.equal(ref[2], a.step(slots, q, k, v, alpha, beta)[2])
 
 
+def test_memory_kept_by_an_object_outlives_its_streams_work():
+    """What a call on another stream still uses is not handed to the next allocation."""
+    side, dev = torch.cuda.Stream(), torch.device("cuda")
+    from ssm_decode_step_b200 import StateCache
+    cfg = _cfg(4, 8, 64, 64, 8, 64, 1)
+    slots = torch.arange(4, dtype=torch.int32, device=dev)
+    S = torch.ones(4, 8, 64, 64, device=dev)
+    cache = StateCache(cfg, 8)
+    kept = cache.codes.data_ptr()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    cache.write(slots, S, stream=side)
+    del cache
+    assert torch.empty(4 * 8 * 64 * 64, dtype=torch.uint8, device=dev).data_ptr() != kept
+    torch.cuda.synchronize()
+
+
 def test_refusals_of_the_python_calls():
     cfg = _cfg(4, 2, 64, 32, 8, 32)
     from ssm_decode_step_b200 import QStateError, StateCache
