@@ -50,9 +50,9 @@
 // for all, and loops of 16 to 32 columns a turn.  At an item's ends the
 // state's rows pass through the load/store unit (some 4000 cycles of 128 x
 // 128).  Measured on a B200: one prompt of 16384 tokens, 16 heads of 128 x
-// 128, bf16, 115 us (floor of its bytes 42 us); 64 prompts of 256 tokens 90 us
+// 128, bf16, 119 us (floor of its bytes 42 us); 64 prompts of 256 tokens 98 us
 // (62); 32 ragged fp16 prompts, 12000 tokens, 64 heads of 64 x 128 on 8 q/k
-// heads, 288 us (59).
+// heads, 286 us (59).
 #pragma once
 
 #include <cuda.h>
@@ -200,23 +200,27 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Wait for the phase of the given parity; false where it does not complete in
-// kPtPolls looks.  The loop is written out so that it stays this short: a role
-// waits some five times a chunk, and what a wait costs beyond the event counts.
-constexpr uint32_t kPtPolls = 1u << 18;
-__device__ __forceinline__ bool mbar_wait_or_fail(uint32_t bar, uint32_t parity) {
+// One look at the phase of the given parity.
+__device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n\t"
-      "WAIT:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-      "add.u32 n, n, 1;\n\tsetp.lt.u32 p, n, %3;\n\t@p bra WAIT;\n\tsetp.ne.u32 p, n, n;\n\t"
-      "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(done)
-      : "r"(bar), "r"(parity), "n"(kPtPolls)
+      : "r"(bar), "r"(parity)
       : "memory");
   return done != 0;
 }
-
+// Wait for that phase; false where it does not complete in kPtPolls looks.  A
+// role waits some five times a chunk, and what a wait costs beyond the event
+// counts: the loop written in assembly takes 1 to 2% longer, one lane looking for its warp 50% and more.
+constexpr uint32_t kPtPolls = 1u << 18;
+__device__ __forceinline__ bool mbar_wait_or_fail(uint32_t bar, uint32_t parity) {
+  uint32_t polls = 0;
+#pragma unroll 1
+  while (!mbar_done(bar, parity))
+    if (++polls >= kPtPolls) return false;
+  return true;
+}
 __device__ __forceinline__ void mma16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
